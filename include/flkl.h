@@ -31,7 +31,9 @@
  * (selective log-probability), the Jensen-Shannon divergence against a
  * teacher head, a data-parallel form (whole-batch divisor), RMSNorm /
  * LayerNorm backward with frozen-parameter flags, an allocation-free variant,
- * workspace sizes, status and wait-limit helpers.
+ * the scoring path of a head in 8 bits (RMSNorm with the residual's addition
+ * and e4m3 output, block-scaled e4m3 product, token log-probabilities with
+ * entropy and alternatives), workspace sizes, status and wait-limit helpers.
  *
  * Conventions for every entry point:
  *  - Pointers named "device" are CUDA device pointers on the current device;
@@ -398,6 +400,113 @@ FLKL_API flkl_status flkl_layer_norm_backward(const void* dY, const void* X, con
                                               int compute_dW, int compute_db, int accum_fp32,
                                               void* dX, void* dW, void* db, void* workspace,
                                               size_t workspace_bytes, void* stream);
+/* RMSNorm of h = X + residual, with h passed on (the residual stream) and y in
+ * `dtype` or in e4m3 with one fp32 scale per row and 128 columns.  The pages
+ * hold only the norm's backward; this is the forward that stands before the
+ * vocabulary head, in training and (8 bits) where the head is served.
+ *
+ *   h = round(X + residual),  y = W h / sqrt(mean(h^2) + eps)
+ *   scale[r][j] = max |y[r][128 j ..]| / 448,  code = e4m3(y / scale)
+ *
+ *  X, residual  device [rows, H], W [H], `dtype`; residual may be NULL, then
+ *               h = X and Hs must be NULL.
+ *  rows, H, eps as below (flkl_rms_norm_backward), rows below 2^31.
+ *  quantize     nonzero: Y holds e4m3 codes (one byte each) and scale is
+ *               written; zero: Y has `dtype` and scale must be NULL.
+ *  Y            device [rows, H] (overwritten).
+ *  scale        device fp32 [rows, ceil(H / 128)]; a block below 2^-100
+ *               throughout has scale 1 and codes 0.
+ *  Hs           device [rows, H], `dtype`: h; may be X or residual (in place).
+ *  Pointers 16-byte aligned (scale 4).  Asynchronous on `stream`; no
+ *  workspace; host-side errors as flkl_forward_backward.
+ *
+ * flkl_add_rms_norm_backward: dX = dH + d y / d h (dY), the gradient of X and
+ * of residual alike, from Hs (the forward's h; X where there was no residual)
+ * and dH, the gradient that arrives at h from its other use (NULL: none).
+ * Other arguments, dW, workspace and status as flkl_rms_norm_backward. */
+FLKL_API flkl_status flkl_add_rms_norm_forward(const void* X, const void* residual, const void* W,
+                                               int64_t rows, int64_t H, int dtype, float eps,
+                                               int quantize, void* Y, float* scale, void* Hs,
+                                               void* stream);
+FLKL_API flkl_status flkl_add_rms_norm_backward(const void* dY, const void* dH, const void* Hs,
+                                                const void* W, int64_t rows, int64_t H,
+                                                int dtype, float eps, int compute_dW,
+                                                int accum_fp32, void* dX, void* dW,
+                                                void* workspace, size_t workspace_bytes,
+                                                void* stream);
+
+/* e4m3 codes with fp32 scales of a dense [rows, cols] matrix: one scale per
+ * row and 128 columns (block_rows = 1, activations) or per 128 x 128 block
+ * (block_rows = 128, weights): scale = max |src| over the block / 448, code =
+ * e4m3(src / scale), rounded to nearest even; the last block of a row or
+ * column may be short.
+ *  src    device [rows, cols], `dtype`; cols a multiple of 16.
+ *  q      device [rows, cols] bytes (overwritten).
+ *  scale  device fp32 [ceil(rows / block_rows), ceil(cols / 128)].
+ *  src and q 16-byte aligned.  Asynchronous on `stream`. */
+FLKL_API flkl_status flkl_fp8_quantize(const void* src, int64_t rows, int64_t cols, int dtype,
+                                       int block_rows, void* q, float* scale, void* stream);
+
+/* Product of two e4m3 matrices with a scale per block of 128 (the vocabulary
+ * head, or any projection, in 8 bits):
+ *
+ *   D[m][n] = sum_kb a_scale[m][kb] b_scale[n / 128][kb]
+ *                  sum_{k in block kb} A[m][k] B[n][k]  (+ bias[n])
+ *
+ *  A        device [M, K] e4m3, a_scale fp32 [M, ceil(K / 128)].
+ *  B        device [N, K] e4m3, b_scale fp32 [ceil(N / 128), ceil(K / 128)].
+ *  bias     device [N], out_dtype, or NULL.
+ *  D        device [M, N], out_dtype (overwritten), sums in fp32.
+ *  M, N >= 0, K >= 1 a multiple of 16, each below 2^31; A and B 16-byte
+ *  aligned, the others to their type; all dense.  Asynchronous on `stream`;
+ *  no workspace. */
+FLKL_API flkl_status flkl_fp8_block_matmul(const void* A, const float* a_scale, const void* B,
+                                           const float* b_scale, const void* bias, int64_t M,
+                                           int64_t N, int64_t K, int out_dtype, void* D,
+                                           void* stream);
+
+/* Log-probabilities of given tokens, entropy and best alternatives of rows of
+ * logits (where logits exist: a served or scored batch, a head that is not
+ * this library's; flkl_selective_logprob_forward needs none).  With
+ * u = logits / temperature, p = softmax(u) over the row:
+ *
+ *   lse = ln sum exp u,  logp[r] = u[target[r]] - lse,  entropy = -sum p ln p,
+ *   top_ids[r] = the top_k largest logits, ties to the lower index, and
+ *   top_logp[r] their u - lse.
+ *
+ *  logits      device, `dtype`, rows of V values row_stride elements apart
+ *              (>= V); any alignment of `dtype`.
+ *  target      device int64 [rows], or NULL (then logp NULL).  A row whose
+ *              target is ignore_index is dropped: logp, entropy, lse and
+ *              top_logp 0, top_ids -1, gradient 0, its logits not read.  A
+ *              target outside [0, V) otherwise: logp 0, the rest as usual.
+ *  top_k       0 .. 32, at most V.
+ *  entropy, lse   device fp32 [rows]; logp likewise (with target).
+ *  stats       device fp32 [rows, 2], 8-byte aligned: the row's largest logit
+ *              and ln sum exp(u - max u), for the backward call.
+ *  top_logp    device fp32 [rows, top_k], top_ids device int64 (top_k > 0).
+ *  Logits of -infinity have probability 0; a row of nothing else gives
+ *  entropy 0, logp, lse and top_logp -infinity, gradient 0.  A row that holds
+ *  NaN or +infinity gives NaN (top_ids: NaN first, then by value).
+ *  Deterministic; no workspace.
+ *
+ * flkl_token_logprobs_backward: the gradient of the logits for upstream
+ * gradients dlogp, dentropy [rows] and dtop_logp [rows, top_k] (device fp32,
+ * NULL: none), from the forward's stats, entropy and top_ids; the other
+ * arguments are the forward's.  dlogits: `dtype`, rows d_row_stride apart. */
+FLKL_API flkl_status flkl_token_logprobs_forward(const void* logits, int64_t row_stride,
+                                                 const int64_t* target, int64_t ignore_index,
+                                                 int64_t rows, int64_t V, int dtype,
+                                                 float temperature, int top_k, float* logp,
+                                                 float* entropy, float* lse, float* stats,
+                                                 float* top_logp, int64_t* top_ids,
+                                                 void* stream);
+FLKL_API flkl_status flkl_token_logprobs_backward(
+    const void* logits, int64_t row_stride, const int64_t* target, int64_t ignore_index,
+    int64_t rows, int64_t V, int dtype, float temperature, int top_k, const float* stats,
+    const float* entropy, const int64_t* top_ids, const float* dlogp, const float* dentropy,
+    const float* dtop_logp, void* dlogits, int64_t d_row_stride, void* stream);
+
 /* Synchronises `stream` and returns the status word of the norm-backward
  * kernels of the current device (FLKL_OK, or FLKL_ERR_TIMEOUT when one of
  * their waits gave up since the last call), then clears it. */

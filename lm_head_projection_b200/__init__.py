@@ -28,6 +28,8 @@ __all__ = [
     "flkl_jsd_workspace_size", "flkl_jsd_forward_backward", "jsd_forward_backward",
     "FusedLinearJSDLoss", "flkl_scale_cast", "flkl_clock_trace", "flkl_gemm_ctas", "flkl_vocab_chunks",
     "flkl_forward_backward_dp_events", "flkl_ce_forward_backward_dp_events",
+    "flkl_add_rms_norm_forward", "flkl_add_rms_norm_backward", "flkl_fp8_quantize",
+    "flkl_fp8_block_matmul", "flkl_token_logprobs_forward", "flkl_token_logprobs_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -151,6 +153,22 @@ def _lib():
             c.c_void_p, c.c_void_p, c.c_void_p, c.c_int64, c.c_int64, c.c_int, c.c_float,
             c.c_int, c.c_int, c.c_int, c.c_void_p, c.c_void_p, c.c_void_p, c.c_void_p,
             c.c_size_t, c.c_void_p]
+        P, I, L, F = c.c_void_p, c.c_int, c.c_int64, c.c_float
+        lib.flkl_add_rms_norm_forward.restype = I
+        lib.flkl_add_rms_norm_forward.argtypes = [P, P, P, L, L, I, F, I, P, P, P, P]
+        lib.flkl_add_rms_norm_backward.restype = I
+        lib.flkl_add_rms_norm_backward.argtypes = [P, P, P, P, L, L, I, F, I, I, P, P, P,
+                                                   c.c_size_t, P]
+        lib.flkl_fp8_quantize.restype = I
+        lib.flkl_fp8_quantize.argtypes = [P, L, L, I, I, P, P, P]
+        lib.flkl_fp8_block_matmul.restype = I
+        lib.flkl_fp8_block_matmul.argtypes = [P, P, P, P, P, L, L, L, I, P, P]
+        lib.flkl_token_logprobs_forward.restype = I
+        lib.flkl_token_logprobs_forward.argtypes = [P, L, P, L, L, L, I, F, I, P, P, P, P, P, P,
+                                                    P]
+        lib.flkl_token_logprobs_backward.restype = I
+        lib.flkl_token_logprobs_backward.argtypes = [P, L, P, L, L, L, I, F, I, P, P, P, P, P, P,
+                                                     P, L, P]
         _LIB = lib
     return _LIB
 
@@ -280,6 +298,51 @@ def flkl_layer_norm_backward(dY, X, W, rows, H, dtype, eps, compute_dW, compute_
         int(workspace_bytes), stream)
 
 
+def flkl_add_rms_norm_forward(X, residual, W, rows, H, dtype, eps, quantize, Y, scale, Hs,
+                              stream) -> int:
+    """RMSNorm of X + residual (raw pointers); returns the status."""
+    return _lib().flkl_add_rms_norm_forward(X, residual, W, rows, H, dtype, eps, quantize, Y,
+                                            scale, Hs, stream)
+
+
+def flkl_add_rms_norm_backward(dY, dH, Hs, W, rows, H, dtype, eps, compute_dW, accum_fp32, dX,
+                               dW, workspace, workspace_bytes, stream) -> int:
+    """Its gradient, dH added (raw pointers); returns the status."""
+    return _lib().flkl_add_rms_norm_backward(dY, dH, Hs, W, rows, H, dtype, eps,
+                                             int(bool(compute_dW)), int(bool(accum_fp32)), dX, dW,
+                                             workspace, workspace_bytes, stream)
+
+
+def flkl_fp8_quantize(src, rows, cols, dtype, block_rows, q, scale, stream) -> int:
+    """e4m3 codes and scales (raw pointers); returns the status."""
+    return _lib().flkl_fp8_quantize(src, rows, cols, dtype, block_rows, q, scale, stream)
+
+
+def flkl_fp8_block_matmul(A, a_scale, B, b_scale, bias, M, N, K, out_dtype, D, stream) -> int:
+    """The block-scaled e4m3 product (raw pointers); returns the status."""
+    return _lib().flkl_fp8_block_matmul(A, a_scale, B, b_scale, bias, M, N, K, out_dtype, D,
+                                        stream)
+
+
+def flkl_token_logprobs_forward(logits, row_stride, target, ignore_index, rows, V, dtype,
+                                temperature, top_k, logp, entropy, lse, stats, top_logp, top_ids,
+                                stream) -> int:
+    """Token log-probabilities of rows of logits (raw pointers); returns the status."""
+    return _lib().flkl_token_logprobs_forward(logits, row_stride, target, ignore_index, rows, V,
+                                              dtype, temperature, top_k, logp, entropy, lse,
+                                              stats, top_logp, top_ids, stream)
+
+
+def flkl_token_logprobs_backward(logits, row_stride, target, ignore_index, rows, V, dtype,
+                                 temperature, top_k, stats, entropy, top_ids, dlogp, dentropy,
+                                 dtop_logp, dlogits, d_row_stride, stream) -> int:
+    """The logits' gradient (raw pointers); returns the status."""
+    return _lib().flkl_token_logprobs_backward(logits, row_stride, target, ignore_index, rows, V,
+                                               dtype, temperature, top_k, stats, entropy,
+                                               top_ids, dlogp, dentropy, dtop_logp, dlogits,
+                                               d_row_stride, stream)
+
+
 def flkl_norm_device_status(stream=None) -> int:
     """Synchronise ``stream``; status of the norm kernels since the last call."""
     return _lib().flkl_norm_device_status(stream)
@@ -400,6 +463,21 @@ def _check_dev(name, t, dtype, shape, device):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _launch(what: str, call, args, dev, stream: Optional[torch.cuda.Stream]) -> None:
+    """``call(*args, stream)`` on ``stream`` (default: the current one of
+    ``dev``) with ``dev`` as the current device, since the library launches
+    there; raises FlklError on a non-OK status."""
+    if dev.type != "cuda":
+        raise ValueError(f"{what} needs CUDA tensors, got {dev}")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _launch(what, call, args, dev, stream)
+    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    status = call(*args, st.cuda_stream)
+    if status != FLKL_OK:
+        raise FlklError(status, what)
 
 
 def _outputs(out: Optional[dict], dev, BT: int, H: int, V: int, dt, pdt, compute_dW: bool,

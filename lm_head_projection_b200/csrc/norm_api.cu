@@ -5,6 +5,7 @@
 
 #include "../../include/flkl.h"
 #include "norm_bwd.cuh"
+#include "norm_fwd.cuh"
 
 namespace flkl {
 
@@ -62,7 +63,7 @@ struct NormCfg {
 // registers allow, then as many stages (>= min_stages) as their share of
 // shared memory holds, fewer CTAs when that many stages do not fit.
 template <typename K>
-NormCfg pick_config(K kern, int NT, int H, size_t elem, int min_stages) {
+NormCfg pick_config(K kern, int NT, int H, size_t elem, int min_stages, int n_in) {
   static std::mutex mu;
   struct Entry {
     const void* k;
@@ -86,14 +87,14 @@ NormCfg pick_config(K kern, int NT, int H, size_t elem, int min_stages) {
     return c;
   const size_t row = static_cast<size_t>(H) * elem;
   int by_regs = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&by_regs, kern, NT, 3 * row) !=
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&by_regs, kern, NT, (1 + n_in) * row) !=
           cudaSuccess ||
       by_regs < 1)
     return c;
   for (int n = by_regs; n >= 1; --n) {
     const long long budget = kSmemPerSm / n - kSmemPerCtaReserved - static_smem;
     const long long cap = std::min<long long>(budget, kMaxCtaSmem - static_smem);
-    const long long st = (cap / static_cast<long long>(row) - 1) / 2;
+    const long long st = (cap / static_cast<long long>(row) - 1) / n_in;
     if (st >= min_stages) {
       c.stages = static_cast<int>(std::min<long long>(st, kNormMaxStages));
       c.ctas_per_sm = n;
@@ -103,7 +104,7 @@ NormCfg pick_config(K kern, int NT, int H, size_t elem, int min_stages) {
   if (c.stages >= min_stages) {
     int occ = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-            &occ, kern, NT, static_cast<size_t>(row) * (1 + 2 * c.stages)) != cudaSuccess ||
+            &occ, kern, NT, static_cast<size_t>(row) * (1 + n_in * c.stages)) != cudaSuccess ||
         occ < 1)
       c = NormCfg{};
     else
@@ -113,7 +114,7 @@ NormCfg pick_config(K kern, int NT, int H, size_t elem, int min_stages) {
   return c;
 }
 
-template <typename T, int LAYER, int NT, int VPT, int R, bool CW, bool CB>
+template <typename T, int LAYER, int NT, int VPT, int R, bool CW, bool CB, bool ADD>
 flkl_status launch_r(NormArgs a, const NormCfg& c, int64_t max_ctas, cudaStream_t st,
                      int* n_ctas) {
   const int64_t grid = std::min<int64_t>({(CW || CB) ? max_ctas : a.rows,
@@ -121,39 +122,48 @@ flkl_status launch_r(NormArgs a, const NormCfg& c, int64_t max_ctas, cudaStream_
                                           a.rows});
   a.stages = c.stages;
   *n_ctas = static_cast<int>(grid);
-  k_norm_bwd<T, LAYER, NT, VPT, R, CW, CB>
-      <<<static_cast<unsigned>(grid), NT, norm_smem_bytes<T>(a.H, c.stages), st>>>(a);
+  k_norm_bwd<T, LAYER, NT, VPT, R, CW, CB, ADD>
+      <<<static_cast<unsigned>(grid), NT, norm_smem_bytes<T>(a.H, c.stages, ADD ? 3 : 2), st>>>(a);
   return cudaGetLastError() == cudaSuccess ? FLKL_OK : FLKL_ERR_CUDA;
 }
 
 // R rows per iteration where 2 R stages fit, else one.
-template <typename T, int LAYER, int NT, int VPT, int R, bool CW, bool CB>
+template <typename T, int LAYER, int NT, int VPT, int R, bool CW, bool CB, bool ADD>
 flkl_status launch_one(const NormArgs& a, int64_t max_ctas, cudaStream_t st, int* n_ctas) {
-  const NormCfg c = pick_config(k_norm_bwd<T, LAYER, NT, VPT, R, CW, CB>, NT, a.H, sizeof(T),
-                                2 * R);
+  const NormCfg c = pick_config(k_norm_bwd<T, LAYER, NT, VPT, R, CW, CB, ADD>, NT, a.H,
+                                sizeof(T), 2 * R, ADD ? 3 : 2);
   if (c.stages >= 2 * R)
-    return launch_r<T, LAYER, NT, VPT, R, CW, CB>(a, c, max_ctas, st, n_ctas);
-  if constexpr (R > 1) return launch_one<T, LAYER, NT, VPT, 1, CW, CB>(a, max_ctas, st, n_ctas);
+    return launch_r<T, LAYER, NT, VPT, R, CW, CB, ADD>(a, c, max_ctas, st, n_ctas);
+  if constexpr (R > 1)
+    return launch_one<T, LAYER, NT, VPT, 1, CW, CB, ADD>(a, max_ctas, st, n_ctas);
   return FLKL_ERR_CUDA;
 }
 
-template <typename T, int LAYER, int NT, int VPT, int R>
+template <typename T, int LAYER, int NT, int VPT, int R, bool ADD>
 flkl_status launch_flags(const NormArgs& a, int64_t max_ctas, cudaStream_t st, int* n) {
   if constexpr (LAYER) {
     if (a.part_w && a.part_b)
-      return launch_one<T, 1, NT, VPT, R, true, true>(a, max_ctas, st, n);
-    if (a.part_b) return launch_one<T, 1, NT, VPT, R, false, true>(a, max_ctas, st, n);
+      return launch_one<T, 1, NT, VPT, R, true, true, false>(a, max_ctas, st, n);
+    if (a.part_b) return launch_one<T, 1, NT, VPT, R, false, true, false>(a, max_ctas, st, n);
   }
-  if (a.part_w) return launch_one<T, LAYER, NT, VPT, R, true, false>(a, max_ctas, st, n);
-  return launch_one<T, LAYER, NT, VPT, R, false, false>(a, max_ctas, st, n);
+  if (a.part_w) return launch_one<T, LAYER, NT, VPT, R, true, false, ADD>(a, max_ctas, st, n);
+  return launch_one<T, LAYER, NT, VPT, R, false, false, ADD>(a, max_ctas, st, n);
 }
 
 // Threads, vectors per thread and rows per iteration by row width.
-template <typename T, int LAYER>
+template <typename T, int LAYER, bool ADD>
 flkl_status launch_norm(const NormArgs& a, int64_t max_ctas, cudaStream_t st, int* n) {
-  if (a.H <= 2048) return launch_flags<T, LAYER, 128, 2, 1>(a, max_ctas, st, n);
-  if (a.H <= 4096) return launch_flags<T, LAYER, 128, 4, 1>(a, max_ctas, st, n);
-  return launch_flags<T, LAYER, 256, 4, 1>(a, max_ctas, st, n);
+  if (a.H <= 2048) return launch_flags<T, LAYER, 128, 2, 1, ADD>(a, max_ctas, st, n);
+  if (a.H <= 4096) return launch_flags<T, LAYER, 128, 4, 1, ADD>(a, max_ctas, st, n);
+  return launch_flags<T, LAYER, 256, 4, 1, ADD>(a, max_ctas, st, n);
+}
+
+// kind: 0 RMSNorm, 1 LayerNorm, 2 RMSNorm with the gradient dH added to dX.
+template <typename T>
+flkl_status launch_kind(int kind, const NormArgs& a, int64_t max_ctas, cudaStream_t st, int* n) {
+  if (kind == 2) return launch_norm<T, 0, true>(a, max_ctas, st, n);
+  return kind == 1 ? launch_norm<T, 1, false>(a, max_ctas, st, n)
+                   : launch_norm<T, 0, false>(a, max_ctas, st, n);
 }
 
 int* norm_status_ptr() {
@@ -168,8 +178,8 @@ int* norm_status_ptr() {
   return cache[dev];
 }
 
-flkl_status norm_backward(int layer, const void* dY, const void* X, const void* W, int64_t rows,
-                          int64_t H, int dtype, float eps, int compute_dW, int compute_db,
+flkl_status norm_backward(int kind, const void* dY, const void* dH, const void* X, const void* W,
+                          int64_t rows, int64_t H, int dtype, float eps, int compute_dW, int compute_db,
                           int accum_fp32, void* dX, void* dW, void* db, void* workspace,
                           size_t workspace_bytes, void* stream) {
   if (dtype != FLKL_DTYPE_F32 && dtype != FLKL_DTYPE_BF16) return FLKL_ERR_INVALID_ARG;
@@ -179,7 +189,7 @@ flkl_status norm_backward(int layer, const void* dY, const void* X, const void* 
     return FLKL_ERR_INVALID_ARG;
   if ((compute_dW != 0) != (dW != nullptr) || (compute_db != 0) != (db != nullptr))
     return FLKL_ERR_INVALID_ARG;
-  if (!al16(dY) || !al16(X) || !al16(W) || !al16(dX) || !al16(dW) || !al16(db))
+  if (!al16(dY) || !al16(dH) || !al16(X) || !al16(W) || !al16(dX) || !al16(dW) || !al16(db))
     return FLKL_ERR_UNSUPPORTED;
   const size_t need = flkl_norm_workspace_size(rows, H, compute_dW, compute_db);
   if (need > 0 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
@@ -189,6 +199,7 @@ flkl_status norm_backward(int layer, const void* dY, const void* X, const void* 
   const int64_t max_ctas = norm_max_ctas(rows, H);
   NormArgs a{};
   a.dY = dY;
+  a.dH = dH;
   a.X = X;
   a.W = W;
   a.rows = rows;
@@ -204,10 +215,8 @@ flkl_status norm_backward(int layer, const void* dY, const void* X, const void* 
   int n_ctas = 0;
   if (rows > 0) {
     const flkl_status s = dtype == FLKL_DTYPE_BF16
-        ? (layer ? launch_norm<__nv_bfloat16, 1>(a, max_ctas, st, &n_ctas)
-                 : launch_norm<__nv_bfloat16, 0>(a, max_ctas, st, &n_ctas))
-        : (layer ? launch_norm<float, 1>(a, max_ctas, st, &n_ctas)
-                 : launch_norm<float, 0>(a, max_ctas, st, &n_ctas));
+                              ? launch_kind<__nv_bfloat16>(kind, a, max_ctas, st, &n_ctas)
+                              : launch_kind<float>(kind, a, max_ctas, st, &n_ctas);
     if (s != FLKL_OK) return s;
   }
   const int out_fp32 = (dtype == FLKL_DTYPE_F32 || accum_fp32) ? 1 : 0;
@@ -238,7 +247,7 @@ flkl_status flkl_rms_norm_backward(const void* dY, const void* X, const void* W,
                                    int64_t H, int dtype, float eps, int compute_dW,
                                    int accum_fp32, void* dX, void* dW, void* workspace,
                                    size_t workspace_bytes, void* stream) {
-  return flkl::norm_backward(0, dY, X, W, rows, H, dtype, eps, compute_dW, 0, accum_fp32, dX, dW,
+  return flkl::norm_backward(0, dY, nullptr, X, W, rows, H, dtype, eps, compute_dW, 0, accum_fp32, dX, dW,
                              nullptr, workspace, workspace_bytes, stream);
 }
 
@@ -246,8 +255,48 @@ flkl_status flkl_layer_norm_backward(const void* dY, const void* X, const void* 
                                      int64_t H, int dtype, float eps, int compute_dW,
                                      int compute_db, int accum_fp32, void* dX, void* dW, void* db,
                                      void* workspace, size_t workspace_bytes, void* stream) {
-  return flkl::norm_backward(1, dY, X, W, rows, H, dtype, eps, compute_dW, compute_db,
+  return flkl::norm_backward(1, dY, nullptr, X, W, rows, H, dtype, eps, compute_dW, compute_db,
                              accum_fp32, dX, dW, db, workspace, workspace_bytes, stream);
+}
+
+flkl_status flkl_add_rms_norm_backward(const void* dY, const void* dH, const void* Hs,
+                                       const void* W, int64_t rows, int64_t H, int dtype,
+                                       float eps, int compute_dW, int accum_fp32, void* dX,
+                                       void* dW, void* workspace, size_t workspace_bytes,
+                                       void* stream) {
+  return flkl::norm_backward(dH != nullptr ? 2 : 0, dY, dH, Hs, W, rows, H, dtype, eps, compute_dW,
+                             0, accum_fp32, dX, dW, nullptr, workspace, workspace_bytes, stream);
+}
+
+flkl_status flkl_add_rms_norm_forward(const void* X, const void* residual, const void* W,
+                                      int64_t rows, int64_t H, int dtype, float eps, int quantize,
+                                      void* Y, float* scale, void* Hs, void* stream) {
+  if (dtype != FLKL_DTYPE_F32 && dtype != FLKL_DTYPE_BF16) return FLKL_ERR_INVALID_ARG;
+  if (rows < 0 || H < 1 || !(eps >= 0.f) || !(eps < INFINITY)) return FLKL_ERR_INVALID_ARG;
+  if (H % 8 != 0 || H > flkl::kNormMaxH || rows >= (int64_t(1) << 31)) return FLKL_ERR_UNSUPPORTED;
+  if (W == nullptr || (rows > 0 && (X == nullptr || Y == nullptr))) return FLKL_ERR_INVALID_ARG;
+  if (rows > 0 && (quantize != 0) != (scale != nullptr)) return FLKL_ERR_INVALID_ARG;
+  if (rows > 0 && (residual != nullptr) != (Hs != nullptr)) return FLKL_ERR_INVALID_ARG;
+  using flkl::al16;
+  if (!al16(X) || !al16(residual) || !al16(W) || !al16(Y) || !al16(Hs) ||
+      (reinterpret_cast<uintptr_t>(scale) & 3u))
+    return FLKL_ERR_UNSUPPORTED;
+  if (rows == 0) return FLKL_OK;
+  flkl::NormFwdArgs a{};
+  a.X = X;
+  a.R = residual;
+  a.W = W;
+  a.rows = static_cast<int>(rows);
+  a.H = static_cast<int>(H);
+  a.eps = eps;
+  a.Y = Y;
+  a.scale = scale;
+  a.Hs = Hs;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == FLKL_DTYPE_BF16
+                            ? flkl::launch_norm_fwd<__nv_bfloat16>(a, quantize != 0, st)
+                            : flkl::launch_norm_fwd<float>(a, quantize != 0, st);
+  return e == cudaSuccess ? FLKL_OK : FLKL_ERR_CUDA;
 }
 
 flkl_status flkl_norm_device_status(void* stream) {

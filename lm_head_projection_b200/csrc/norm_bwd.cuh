@@ -7,6 +7,10 @@
 //   LayerNorm: y = w * (x - mu) / s + b,  s = sqrt(var(x) + eps)
 //              dx = (g - mean(g) - xhat * mean(g * xhat)) / s
 //   dW = sum over rows of dy * xhat,  db = sum over rows of dy.
+// ADD (RMSNorm of h = x + residual, whose h is passed on too): the gradient
+// that arrives at h from its other use, dh, is staged as a third row and added
+// to dx before its one rounding; dx is then the gradient of x and of the
+// residual alike.
 //
 // HBM-bound, so the design is about keeping bytes in flight: a persistent
 // CTA owns rows blockIdx.x, blockIdx.x + gridDim.x, ... and streams each row
@@ -24,7 +28,7 @@
 // partial rows stay few next to the input rows.
 #pragma once
 
-#include "ptx.cuh"
+#include "vec8.cuh"
 
 namespace flkl {
 
@@ -34,6 +38,7 @@ struct NormArgs {
   const void* dY;
   const void* X;
   const void* W;
+  const void* dH;  // ADD only
   long long rows;
   int H;
   float eps;
@@ -45,48 +50,15 @@ struct NormArgs {
   int stages;                   // 2 .. kNormMaxStages
 };
 
-template <typename T>
-struct Vec8;
-template <>
-struct Vec8<__nv_bfloat16> {
-  __device__ static void load(const __nv_bfloat16* p, float (&f)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    unpack8_bf16(u, f);
-  }
-  __device__ static void store(__nv_bfloat16* p, const float (&f)[8]) {
-    uint4 u;
-    u.x = pack_bf16x2(f[0], f[1]);
-    u.y = pack_bf16x2(f[2], f[3]);
-    u.z = pack_bf16x2(f[4], f[5]);
-    u.w = pack_bf16x2(f[6], f[7]);
-    *reinterpret_cast<uint4*>(p) = u;
-  }
-  __device__ static float first(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-};
-template <>
-struct Vec8<float> {
-  __device__ static void load(const float* p, float (&f)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0];
-    const float4 b = reinterpret_cast<const float4*>(p)[1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  }
-  __device__ static void store(float* p, const float (&f)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-  }
-  __device__ static float first(const float* p) { return *p; }
-};
-
 __device__ __forceinline__ float4 f4add(float4 a, float4 b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
-// Dynamic shared memory: W row, then `stages` x (x row, dy row); each row is
-// H * sizeof(T) bytes, a multiple of 16.
+// Dynamic shared memory: W row, then `stages` x (x row, dy row and, with ADD,
+// dh row: n_in rows); each row is H * sizeof(T) bytes, a multiple of 16.
 template <typename T>
-__host__ __device__ constexpr size_t norm_smem_bytes(int H, int stages) {
-  return static_cast<size_t>(H) * sizeof(T) * (1 + 2 * static_cast<size_t>(stages));
+__host__ __device__ constexpr size_t norm_smem_bytes(int H, int stages, int n_in) {
+  return static_cast<size_t>(H) * sizeof(T) * (1 + n_in * static_cast<size_t>(stages));
 }
 
 // LAYER: 0 RMSNorm, 1 LayerNorm.  NT threads, VPT vectors of 8 columns each
@@ -94,9 +66,10 @@ __host__ __device__ constexpr size_t norm_smem_bytes(int H, int stages) {
 // iteration: their sums share one barrier and their passes interleave, at no
 // extra register cost for the dW / db sums; stages >= 2 * R.
 // CW / CB: accumulate dW / db (frozen ones compile out).
-template <typename T, int LAYER, int NT, int VPT, int R, bool CW, bool CB>
+template <typename T, int LAYER, int NT, int VPT, int R, bool CW, bool CB, bool ADD>
 __global__ void __launch_bounds__(NT) k_norm_bwd(const NormArgs a) {
   constexpr int NW = NT / 32;
+  constexpr int NIN = ADD ? 3 : 2;  // staged rows per stage
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kNormMaxStages];
   __shared__ uint64_t wbar;
@@ -106,19 +79,22 @@ __global__ void __launch_bounds__(NT) k_norm_bwd(const NormArgs a) {
   const int H = a.H;
   const uint32_t row_bytes = static_cast<uint32_t>(H) * sizeof(T);
   const T* w_s = reinterpret_cast<const T*>(smem);
-  auto x_stage = [&](int s) { return reinterpret_cast<T*>(smem + row_bytes * (1 + 2 * s)); };
-  auto dy_stage = [&](int s) { return reinterpret_cast<T*>(smem + row_bytes * (2 + 2 * s)); };
+  auto x_stage = [&](int s) { return reinterpret_cast<T*>(smem + row_bytes * (1 + NIN * s)); };
+  auto dy_stage = [&](int s) { return reinterpret_cast<T*>(smem + row_bytes * (2 + NIN * s)); };
+  auto dh_stage = [&](int s) { return reinterpret_cast<T*>(smem + row_bytes * (3 + NIN * s)); };
   const int S = a.stages;
   const long long step = gridDim.x;
   const long long n_mine =
       blockIdx.x < a.rows ? (a.rows - 1 - blockIdx.x) / step + 1 : 0;
   const T* X = static_cast<const T*>(a.X);
   const T* dY = static_cast<const T*>(a.dY);
+  const T* dH = static_cast<const T*>(a.dH);
   auto issue = [&](int s, long long k) {
     const size_t off = static_cast<size_t>(blockIdx.x + k * step) * H;
-    mbar_arrive_expect_tx(&full[s], 2 * row_bytes);
+    mbar_arrive_expect_tx(&full[s], NIN * row_bytes);
     bulk_load_1d(x_stage(s), X + off, row_bytes, &full[s]);
     bulk_load_1d(dy_stage(s), dY + off, row_bytes, &full[s]);
+    if constexpr (ADD) bulk_load_1d(dh_stage(s), dH + off, row_bytes, &full[s]);
   };
   // Rows issued when the barrier of the iteration starting at row k is
   // reached: 0 .. S-1 at first, then the previous iteration's rows + S at
@@ -279,14 +255,16 @@ __global__ void __launch_bounds__(NT) k_norm_bwd(const NormArgs a) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         if (col(v) >= H) continue;
-        float x[8], dy[8], wv[8], o[8];
+        float x[8], dy[8], wv[8], o[8], dh[8];
         Vec8<T>::load(x_stage(s) + col(v), x);
         Vec8<T>::load(dy_stage(s) + col(v), dy);
+        if constexpr (ADD) Vec8<T>::load(dh_stage(s) + col(v), dh);
         get_w(v, wv);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float xh = fmaf(x[i], rinv, bx);
           o[i] = fmaf(dy[i] * wv[i], rinv, -fmaf(xh, c2r, gmr));
+          if constexpr (ADD) o[i] += dh[i];
           if constexpr (CW) accw[v][i] = fmaf(dy[i], xh, accw[v][i]);
           if constexpr (CB) accb[v][i] += dy[i];
         }

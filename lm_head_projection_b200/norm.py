@@ -1,4 +1,5 @@
-"""RMSNorm / LayerNorm backward with frozen-parameter flags.
+"""RMSNorm / LayerNorm backward with frozen-parameter flags, and RMSNorm with
+the residual's addition.
 
 The LoRA normalization pull-request page (*Key Changes*): when a norm's
 weight (bias) is frozen, its gradient is neither accumulated nor reduced;
@@ -6,6 +7,13 @@ the input gradient does not change.  ``rms_norm_backward`` and
 ``layer_norm_backward`` marshal torch tensors into the C entry points
 ``flkl_rms_norm_backward`` / ``flkl_layer_norm_backward``; the autograd
 modules below take the flags from ``requires_grad`` of the parameters.
+
+``add_rms_norm`` is the norm that stands before the vocabulary head (and
+before any projection of a residual network): h = X + residual, y = W h /
+rms(h), with h passed on and y in the input's type or in e4m3 with one scale
+per row and 128 columns, as :func:`lm_head_projection_b200.fp8.block_matmul`
+reads it; ``add_rms_norm_backward`` and the module ``AddRMSNorm`` differentiate
+the former.
 There is no PyTorch fallback: the CUDA library does every step.
 """
 
@@ -15,10 +23,12 @@ from typing import Optional
 
 import torch
 
-from . import (DTYPES, FLKL_OK, FlklError, _check_dev, _ptr, flkl_layer_norm_backward,
+from . import (DTYPES, FLKL_OK, FlklError, _check_dev, _launch, _ptr,
+               flkl_add_rms_norm_backward, flkl_add_rms_norm_forward, flkl_layer_norm_backward,
                flkl_norm_workspace_size, flkl_rms_norm_backward)
 
-__all__ = ["rms_norm_backward", "layer_norm_backward", "RMSNorm", "LayerNorm"]
+__all__ = ["rms_norm_backward", "layer_norm_backward", "RMSNorm", "LayerNorm", "add_rms_norm",
+           "add_rms_norm_backward", "AddRMSNorm"]
 
 
 def _prepare(dY, X, W, accum_fp32):
@@ -74,6 +84,83 @@ def layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, eps:
     if status != FLKL_OK:
         raise FlklError(status, "flkl_layer_norm_backward")
     return {"dX": dX, "dW": dW, "db": db}
+
+
+def add_rms_norm(X: torch.Tensor, W: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, quantize: bool = False, inplace: bool = False,
+                 stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """``h = X + residual`` (rounded to the inputs' type), ``y = W * h / rms(h)``
+    over the last dimension, in one pass; returns ``{"Y", "scale", "H"}``.
+
+    ``quantize`` gives Y as ``torch.float8_e4m3fn`` codes with fp32 scales
+    ``[..., ceil(H / 128)]`` (largest magnitude of 128 columns / 448); else Y
+    has X's type and scale is None.  Without a residual H is X itself;
+    ``inplace`` writes h over the residual.  No gradient is recorded: see
+    :class:`AddRMSNorm`."""
+    if X.dtype not in DTYPES:
+        raise ValueError(f"dtype {X.dtype} not supported (float32 or bfloat16)")
+    if X.dim() < 1:
+        raise ValueError("X needs a last (hidden) dimension")
+    H = X.shape[-1]
+    rows = X.numel() // H if H else 0
+    dev, dt = X.device, X.dtype
+    _check_dev("X", X, dt, X.shape, dev)
+    _check_dev("W", W, dt, (H,), dev)
+    Hs = None
+    if residual is not None:
+        _check_dev("residual", residual, dt, X.shape, dev)
+        Hs = residual.detach() if inplace else torch.empty_like(X)
+    elif inplace:
+        raise ValueError("inplace needs a residual")
+    Y = torch.empty(X.shape, dtype=torch.float8_e4m3fn if quantize else dt, device=dev)
+    scale = torch.empty((*X.shape[:-1], -(-H // 128)), dtype=torch.float32, device=dev) \
+        if quantize else None
+    _launch("flkl_add_rms_norm_forward", flkl_add_rms_norm_forward,
+            (X.data_ptr(), _ptr(residual), W.data_ptr(), rows, H, DTYPES[dt], eps,
+             int(bool(quantize)), Y.data_ptr(), _ptr(scale), _ptr(Hs)), dev, stream)
+    return {"Y": Y, "scale": scale, "H": X if Hs is None else Hs}
+
+
+def add_rms_norm_backward(dY: torch.Tensor, H: torch.Tensor, W: torch.Tensor,
+                          dH: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                          compute_dW: bool = True, accum_fp32: bool = True,
+                          stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """Gradients of :func:`add_rms_norm` from its ``H``: dX, the gradient of X
+    and of the residual alike, with ``dH`` (what arrives at h from its other
+    use) added; and dW unless the weight is frozen.  Returns ``{"dX", "dW"}``."""
+    rows, hidden, dev, dt, pdt = _prepare(dY, H, W, accum_fp32)
+    if dH is not None:
+        _check_dev("dH", dH, dt, H.shape, dev)
+    dX = torch.empty_like(H)
+    dW = torch.empty((hidden,), dtype=pdt, device=dev) if compute_dW else None
+    with torch.cuda.device(dev):  # the size goes by the current device
+        need = flkl_norm_workspace_size(rows, hidden, compute_dW, False)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _launch("flkl_add_rms_norm_backward", flkl_add_rms_norm_backward,
+            (_ptr(dY), _ptr(dH), _ptr(H), _ptr(W), rows, hidden, DTYPES[dt], eps, compute_dW,
+             accum_fp32, _ptr(dX), _ptr(dW), _ptr(ws), need), dev, stream)
+    return {"dX": dX, "dW": dW}
+
+
+class _AddRMSNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, residual, W, eps):
+        r = add_rms_norm(X, W, residual, eps)
+        ctx.save_for_backward(r["H"], W)
+        ctx.eps = eps
+        ctx.set_materialize_grads(False)
+        return r["Y"], r["H"]
+
+    @staticmethod
+    def backward(ctx, dY, dH):
+        H, W = ctx.saved_tensors
+        if dY is None:
+            return dH, dH, None, None
+        r = add_rms_norm_backward(dY.contiguous(), H, W,
+                                  None if dH is None else dH.contiguous(), ctx.eps,
+                                  compute_dW=ctx.needs_input_grad[2])
+        dW = None if r["dW"] is None else r["dW"].to(W.dtype)
+        return r["dX"], r["dX"], dW, None
 
 
 class _RMSNormFunction(torch.autograd.Function):
@@ -138,3 +225,25 @@ class LayerNorm(torch.nn.Module):
 
     def forward(self, x):
         return _LayerNormFunction.apply(x.contiguous(), self.weight, self.bias, self.eps)
+
+
+class AddRMSNorm(torch.nn.Module):
+    """RMSNorm of ``x + residual``: ``forward(x, residual) -> (y, h)`` with
+    gradients (dW skipped for a frozen weight); ``quantized(x, residual=None)
+    -> (codes, scale, h)`` gives y in e4m3 for the 8-bit head, without."""
+
+    def __init__(self, hidden: int, eps: float = 1e-6, dtype=torch.bfloat16, device=None):
+        super().__init__()
+        self.weight = torch.nn.Parameter(torch.ones(hidden, dtype=dtype, device=device))
+        self.eps = eps
+
+    def forward(self, x, residual):
+        return _AddRMSNormFunction.apply(x.contiguous(), residual.contiguous(), self.weight,
+                                         self.eps)
+
+    @torch.no_grad()
+    def quantized(self, x, residual=None):
+        r = add_rms_norm(x.contiguous(), self.weight,
+                         None if residual is None else residual.contiguous(), self.eps,
+                         quantize=True)
+        return r["Y"], r["scale"], r["H"]
