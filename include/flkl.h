@@ -459,11 +459,17 @@ FLKL_API flkl_status flkl_fp8_quantize(const void* src, int64_t rows, int64_t co
  *  D        device [M, N], out_dtype (overwritten), sums in fp32.
  *  M, N >= 0, K >= 1 a multiple of 16, each below 2^31; A and B 16-byte
  *  aligned, the others to their type; all dense.  Asynchronous on `stream`;
- *  no workspace. */
+ *  no workspace.  Every wait in the kernels is bounded: after a timeout D is
+ *  undefined and flkl_fp8_device_status says so. */
 FLKL_API flkl_status flkl_fp8_block_matmul(const void* A, const float* a_scale, const void* B,
                                            const float* b_scale, const void* bias, int64_t M,
                                            int64_t N, int64_t K, int out_dtype, void* D,
                                            void* stream);
+
+/* Synchronises `stream` and returns the status word of the product's kernels
+ * on the current device (FLKL_OK, or FLKL_ERR_TIMEOUT when one of their waits
+ * gave up since the last call), then clears it. */
+FLKL_API flkl_status flkl_fp8_device_status(void* stream);
 
 /* Log-probabilities of given tokens, entropy and best alternatives of rows of
  * logits (where logits exist: a served or scored batch, a head that is not

@@ -29,7 +29,7 @@ __all__ = [
     "FusedLinearJSDLoss", "flkl_scale_cast", "flkl_clock_trace", "flkl_gemm_ctas", "flkl_vocab_chunks",
     "flkl_forward_backward_dp_events", "flkl_ce_forward_backward_dp_events",
     "flkl_add_rms_norm_forward", "flkl_add_rms_norm_backward", "flkl_fp8_quantize",
-    "flkl_fp8_block_matmul", "flkl_token_logprobs_forward", "flkl_token_logprobs_backward",
+    "flkl_fp8_block_matmul", "flkl_fp8_device_status", "flkl_token_logprobs_forward", "flkl_token_logprobs_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -163,6 +163,8 @@ def _lib():
         lib.flkl_fp8_quantize.argtypes = [P, L, L, I, I, P, P, P]
         lib.flkl_fp8_block_matmul.restype = I
         lib.flkl_fp8_block_matmul.argtypes = [P, P, P, P, P, L, L, L, I, P, P]
+        lib.flkl_fp8_device_status.restype = I
+        lib.flkl_fp8_device_status.argtypes = [P]
         lib.flkl_token_logprobs_forward.restype = I
         lib.flkl_token_logprobs_forward.argtypes = [P, L, P, L, L, L, I, F, I, P, P, P, P, P, P,
                                                     P]
@@ -322,6 +324,11 @@ def flkl_fp8_block_matmul(A, a_scale, B, b_scale, bias, M, N, K, out_dtype, D, s
     """The block-scaled e4m3 product (raw pointers); returns the status."""
     return _lib().flkl_fp8_block_matmul(A, a_scale, B, b_scale, bias, M, N, K, out_dtype, D,
                                         stream)
+
+
+def flkl_fp8_device_status(stream=None) -> int:
+    """Synchronise ``stream``; status of the product's kernels since the last call."""
+    return _lib().flkl_fp8_device_status(stream)
 
 
 def flkl_token_logprobs_forward(logits, row_stride, target, ignore_index, rows, V, dtype,

@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "_flkl.so")
 SOURCES = ["flkl_api.cu", "norm_api.cu", "scoring_api.cu"]
 HEADERS = ["ptx.cuh", "tc_gemm.cuh", "row_kernels.cuh", "simt_f32.cuh", "norm_bwd.cuh",
-           "jsd_kernels.cuh", "vec8.cuh", "norm_fwd.cuh", "fp8.cuh", "fp8_kernels.cuh",
+           "jsd_kernels.cuh", "vec8.cuh", "norm_fwd.cuh", "fp8.cuh", "fp8_kernels.cuh", "fp8_gemm.cuh",
            "token_logprobs.cuh"]
 
 

@@ -1,0 +1,615 @@
+// The block-scaled e4m3 product on the tensor cores:
+//
+//   D[m][n] = sum_kb sa[m][kb] sb[n / 128][kb] (A B^T over block kb)[m][n]  (+ bias[n])
+//
+// The scales are arbitrary fp32 numbers, so each block of 128 along K is one
+// product of its own in TMEM (four tcgen05.mma.kind::f8f6f4 of K = 32, the first
+// overwriting), read back while the next block's runs into another TMEM
+// buffer, and added with its scales into fp32 registers.  Rows, columns and
+// the end of K that the tiles overhang are zeros that TMA fills in.
+//
+//   k_fp8_pair    many tokens: 256 tokens x 256 weight rows per CTA pair
+//                 (cta_group::2), a TMEM lane holds one token; bound by the
+//                 tensor cores' rate.
+//   k_fp8_skinny  up to 128 tokens: the weight's rows are the MMA's M side, 128
+//                 per tile, the tokens its N side (16 .. 128 columns), so that
+//                 each weight byte is read once and little of an MMA is
+//                 padding; bound by HBM.
+//
+// Every wait is bounded; on a timeout the CTA stops computing, lets its copies
+// and MMAs land, frees TMEM and returns, and the status word says so.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace flkl {
+
+// 0 or FLKL_ERR_TIMEOUT, read and cleared by flkl_fp8_device_status.
+__device__ int g_fp8_status;
+
+struct Fp8Gemm {
+  const float* sa;   // [M][KB]
+  const float* sb;   // [ceil(N / 128)][KB]
+  const void* bias;  // [N] in D's type, or null
+  void* D;           // [M][N]
+  int M, N, KB;
+  int m_tiles, n_tiles;  // token tiles (k_fp8_pair), weight tiles
+  int vec;               // k_fp8_pair: D's rows start on 16-byte boundaries
+  int stages;            // k_fp8_skinny: ring depth
+  unsigned long long wait_limit_ns;
+};
+
+template <typename T>
+__device__ __forceinline__ T fp8_out(float v);
+template <>
+__device__ __forceinline__ float fp8_out<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 fp8_out<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// ------------------------------------------------------------------ pairs
+// Roles of the 12 warps of each CTA: 0 TMA producer, 1 (which owns the TMEM) and
+// 2 the MMA issuers (even CTA), 4 .. 11 the two column halves of the four TMEM
+// lane quarters.  CTA r stages tokens [128 r, 128 r + 128) and weight rows [128 r,
+// 128 r + 128) of the tile, and holds its tokens' outputs.  Tiles go round the
+// pairs, tokens fastest, so that the pairs at work share weight tiles in L2.
+constexpr int P8_STAGES = 6;
+constexpr int P8_HALF = 128 * 128;  // bytes of tokens (or weight rows) per CTA and stage
+constexpr int P8_STAGE = 2 * P8_HALF;
+constexpr int P8_THREADS = 384;
+constexpr int P8_EPI_WARPS = 8;
+constexpr int P8_OUT = 32 * 128;  // bytes that a warp stages of its outputs
+constexpr int P8_SMEM = P8_STAGES * P8_STAGE + P8_EPI_WARPS * P8_OUT + 256 + 1024;
+
+// Writes 32 rows (one per lane, from row0) of COLS = 128 / sizeof(TO)
+// consecutive outputs from column col: through the warp's shared memory, a
+// row's 16-byte units permuted by the row so that neither side meets a bank
+// twice, and from there in whole row pieces (a lane that stored its own row
+// would touch 32 lines an instruction).
+template <typename TO>
+__device__ __forceinline__ void p8_store(const Fp8Gemm& g, uint8_t* buf, int row0, int col,
+                                         const float* v, int lane) {
+  constexpr int COLS = 128 / sizeof(TO);
+  if (col >= g.N) return;
+  const int lim = min(COLS, g.N - col);
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    uint4 w;
+    if constexpr (sizeof(TO) == 2) {
+      w.x = pack_bf16x2(v[8 * u + 0], v[8 * u + 1]);
+      w.y = pack_bf16x2(v[8 * u + 2], v[8 * u + 3]);
+      w.z = pack_bf16x2(v[8 * u + 4], v[8 * u + 5]);
+      w.w = pack_bf16x2(v[8 * u + 6], v[8 * u + 7]);
+    } else {
+      w = make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]),
+                     __float_as_uint(v[4 * u + 2]), __float_as_uint(v[4 * u + 3]));
+    }
+    *reinterpret_cast<uint4*>(buf + lane * 128 + ((u ^ (lane & 7)) * 16)) = w;
+  }
+  __syncwarp();
+  TO* d0 = static_cast<TO*>(g.D) + static_cast<size_t>(row0) * g.N + col;
+  const int rows = min(32, g.M - row0);
+  if (g.vec) {  // rows start on 16-byte boundaries and hold whole units
+    const int u = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + (lane >> 3);
+      const uint4 w = *reinterpret_cast<const uint4*>(buf + r * 128 + ((u ^ (r & 7)) * 16));
+      if (r < rows && u * (16 / static_cast<int>(sizeof(TO))) < lim)
+        *reinterpret_cast<uint4*>(d0 + static_cast<size_t>(r) * g.N +
+                                  u * (16 / sizeof(TO))) = w;
+    }
+  } else {
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(
+          buf + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4);
+      TO* d = d0 + static_cast<size_t>(r) * g.N;
+      if constexpr (sizeof(TO) == 4) {
+        if (lane < lim) d[lane] = __uint_as_float(w);
+      } else {
+        uint16_t* h = reinterpret_cast<uint16_t*>(d);
+        if ((reinterpret_cast<uintptr_t>(d) & 2) == 0) {
+          if (2 * lane + 1 < lim) *reinterpret_cast<uint32_t*>(h + 2 * lane) = w;
+          else if (2 * lane < lim) h[2 * lane] = static_cast<uint16_t>(w);
+        } else {  // pairs from the second output on; the ends one by one
+          const uint32_t next = __shfl_down_sync(0xffffffffu, w, 1);
+          if (lane < 31 && 2 * lane + 2 < lim)
+            *reinterpret_cast<uint32_t*>(h + 2 * lane + 1) = (w >> 16) | (next << 16);
+          else if (2 * lane + 1 < lim) h[2 * lane + 1] = static_cast<uint16_t>(w >> 16);
+          if (lane == 0) h[0] = static_cast<uint16_t>(w);
+        }
+      }
+    }
+  }
+  __syncwarp();
+}
+
+template <typename TO>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
+    k_fp8_pair(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
+               const __grid_constant__ Fp8Gemm g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* ring = smem;  // stage: tokens, then weight rows
+  uint8_t* outs = ring + P8_STAGES * P8_STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(outs + P8_EPI_WARPS * P8_OUT);  // even CTA's are used
+  uint64_t* empty = full + P8_STAGES;   // each CTA
+  uint64_t* tfull = empty + P8_STAGES;  // [2] each CTA
+  uint64_t* tempty = tfull + 2;         // [2] even CTA's are used
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_cta_rank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int tiles = g.m_tiles * g.n_tiles;  // (below 2^30: checked by the host)
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < P8_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * P8_EPI_WARPS);
+    }
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&mapA);
+    tma_prefetch_desc(&mapB);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl wc{abort_flag, &g_fp8_status, g.wait_limit_ns};
+
+  // registers: 128 (56 + 2 x 224) = 384 x 168, what the block was launched with
+  if (warp < 4) {
+    reg_dealloc<56>();
+    if (warp == 0 && lane == 0) {
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        const int m0 = (t % g.m_tiles) * 256 + static_cast<int>(rank) * 128;
+        const int n0 = (t / g.m_tiles) * 256 + static_cast<int>(rank) * 128;
+        for (int kb = 0; kb < g.KB; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fbar = mapa_shared(smem_u32(&full[stage]), 0);
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * P8_STAGE);
+          uint8_t* dst = ring + stage * P8_STAGE;
+          tma_load_2d_pair(&mapA, fbar, dst, kb * 128, m0);
+          tma_load_2d_pair(&mapB, fbar, dst + P8_HALF, kb * 128, n0);
+          ++issued;
+          if (++stage == P8_STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // every stage this CTA filled has been consumed before it leaves
+      int s = stage;
+      uint32_t ph = phase;
+      for (int i = 0; i < P8_STAGES && i < issued; ++i) {
+        if (--s < 0) {
+          s = P8_STAGES - 1;
+          ph ^= 1u;
+        }
+        mbar_drain_wait(&empty[s], ph, g.wait_limit_ns);
+      }
+    } else if ((warp == 1 || warp == 2) && lane == 0 && leader) {
+      // warp 1 the even blocks, warp 2 the odd: their buffers differ, so nothing
+      // orders the two, and the waits of one pass while the other's MMAs run
+      constexpr uint32_t idesc = idesc_e4m3_f32(256, 256);
+      const uint64_t d0 = smem_desc_sw128(0, 16u, 1024u);
+      const uint64_t hi = d0 & ~uint64_t(0xFFFFFFFFu);
+      const uint32_t r0 = static_cast<uint32_t>(d0) + ((smem_u32(ring) & 0x3FFFFu) >> 4);
+      const uint32_t buf = warp - 1;
+      const long long total =
+          static_cast<long long>((tiles - pair + pairs - 1) / pairs) * g.KB;  // of this pair
+      int stage = buf;
+      uint32_t phase = 0, tphase = 1;
+      for (long long it = buf; it < total; it += 2) {
+        if (!mbar_wait(&full[stage], phase, wc) || !mbar_wait(&tempty[buf], tphase, wc)) break;
+        tc_fence_after();
+        const uint32_t a = r0 + stage * (P8_STAGE >> 4);
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+          tc_mma_pair_f8(tmem + buf * 256, hi | (a + 2 * k), hi | (a + (P8_HALF >> 4) + 2 * k),
+                         idesc, k);
+        tc_commit_pair(&tfull[buf], 0x3);
+        tc_commit_pair(&empty[stage], 0x3);
+        tphase ^= 1u;
+        stage += 2;
+        if (stage >= P8_STAGES) {
+          stage -= P8_STAGES;
+          phase ^= 1u;
+        }
+      }
+      tc_commit_pair(&drain[buf], 0x1);
+      mbar_drain_wait(&drain[buf], 0, g.wait_limit_ns);
+    }
+    __syncwarp();
+  } else {
+    reg_alloc<224>();
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
+    const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
+    const int nb_last = (g.N - 1) / 128;
+    uint8_t* out = outs + (warp - 4) * P8_OUT;
+    uint32_t it = 0;
+    bool ok = true;
+    // a token's scales times its weight block's, four blocks at a time, loaded
+    // while the four before them are used (rows and columns past the end take
+    // the last one's; not stored)
+    const bool vec4 = g.KB % 4 == 0 && (reinterpret_cast<uintptr_t>(g.sa) & 15) == 0 &&
+                      (reinterpret_cast<uintptr_t>(g.sb) & 15) == 0;
+    const float *pa, *pb;
+    int row0, col0;
+    auto place = [&](int t) {
+      const int nt = t / g.m_tiles, mt = t - nt * g.m_tiles;
+      row0 = mt * 256 + static_cast<int>(rank) * 128 + quad * 32;
+      col0 = nt * 256 + half * 128;
+      pa = g.sa + static_cast<size_t>(min(row0 + lane, g.M - 1)) * g.KB;
+      pb = g.sb + static_cast<size_t>(min(nt * 2 + half, nb_last)) * g.KB;
+    };
+    float4 na, nb;
+    auto load4 = [&](int kb) {
+      if (vec4) {
+        na = __ldg(reinterpret_cast<const float4*>(pa + kb));
+        nb = __ldg(reinterpret_cast<const float4*>(pb + kb));
+      } else {
+        const int k1 = min(kb + 1, g.KB - 1), k2 = min(kb + 2, g.KB - 1),
+                  k3 = min(kb + 3, g.KB - 1);
+        na = make_float4(__ldg(pa + kb), __ldg(pa + k1), __ldg(pa + k2), __ldg(pa + k3));
+        nb = make_float4(__ldg(pb + kb), __ldg(pb + k1), __ldg(pb + k2), __ldg(pb + k3));
+      }
+    };
+    if (pair < tiles) {
+      place(pair);
+      load4(0);
+    }
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      const int out_row = row0, out_col = col0;
+      for (int k4 = 0; k4 < g.KB && ok; k4 += 4) {
+        const float s4[4] = {na.x * nb.x, na.y * nb.y, na.z * nb.z, na.w * nb.w};
+        if (k4 + 4 < g.KB) {
+          load4(k4 + 4);
+        } else if (t + pairs < tiles) {
+          place(t + pairs);
+          load4(0);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (k4 + j >= g.KB) break;
+          const uint32_t buf = it & 1;
+          ok = mbar_wait(&tfull[buf], (it >> 1) & 1, wc);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          uint32_t r[2][16];  // one piece on its way while the other is added
+          tmem_ld16_async(tl + buf * 256, r[0]);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            tmem_wait16(r[c & 1]);
+            if (c < 7) {
+              tmem_ld16_async(tl + buf * 256 + (c + 1) * 16, r[(c + 1) & 1]);
+            } else {
+              // the buffer is read: the MMAs may have it back
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster_relaxed(tempty0 + buf * 8);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              acc[16 * c + i] =
+                  fmaf(__uint_as_float(r[c & 1][i]), s4[j], acc[16 * c + i]);
+          }
+          ++it;
+        }
+      }
+      if (ok && out_row < g.M) {
+        if (g.bias != nullptr) {
+          const TO* b = static_cast<const TO*>(g.bias) + out_col;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (out_col + i < g.N) acc[i] += static_cast<float>(b[i]);
+        }
+        constexpr int COLS = 128 / sizeof(TO);
+#pragma unroll
+        for (int c = 0; c < 128 / COLS; ++c)
+          p8_store<TO>(g, out, out_row, out_col + c * COLS, acc + c * COLS, lane);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ----------------------------------------------------------------- skinny
+// 6 warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 2 .. 5 the epilogue,
+// one per TMEM lane quarter (lane = weight row, BN columns = tokens).  The
+// tokens' scales stand in shared memory for the whole call, [kb][BN].  CTAs
+// take tiles of 128 weight rows in turn.  Where there are too few tiles to
+// keep the SMs reading, a cluster of CTAs shares one tile: CTA r takes its
+// r-th part of K, and the parts' fp32 sums are added in rank order through the
+// cluster's shared memory.
+constexpr int S8_THREADS = 192;
+constexpr int S8_W = 128 * 128;  // weight bytes per stage
+constexpr int S8_MAX_STAGES = 16;
+constexpr int S8_BUFS = 4;       // TMEM buffers of BN columns
+constexpr int S8_MAX_CLUSTER = 8;
+
+template <int BN>
+__host__ __device__ constexpr int s8_stage_bytes() { return S8_W + BN * 128; }
+template <int BN>
+__host__ __device__ constexpr int s8_tmem_cols() {  // a power of two
+  int n = 32;
+  while (n < BN * S8_BUFS) n *= 2;
+  return n;
+}
+// Shared memory besides the ring: barriers, the tokens' scales of kbs blocks,
+// alignment.
+template <int BN>
+__host__ __device__ constexpr size_t s8_smem_fixed(size_t kbs) {
+  return (2 * S8_MAX_STAGES + 2 * S8_BUFS + 2) * 8 + 16 + kbs * BN * 4 + 1024;
+}
+
+template <typename TO, int BN>
+__global__ void __launch_bounds__(S8_THREADS, 1)
+    k_fp8_skinny(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapW,
+                 const __grid_constant__ Fp8Gemm g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const int S = g.stages;
+  uint8_t* ring = smem;  // stage: weight rows, then tokens
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + S * s8_stage_bytes<BN>());
+  uint64_t* empty = full + S8_MAX_STAGES;
+  uint64_t* tfull = empty + S8_MAX_STAGES;  // [S8_BUFS]
+  uint64_t* tempty = tfull + S8_BUFS;       // [S8_BUFS]
+  uint64_t* drain = tempty + S8_BUFS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // [this CTA's kb][BN], 16-byte aligned (the barriers before it are an even number)
+  float* xs = reinterpret_cast<float*>(drain + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t cs, rank = cluster_cta_rank();
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cs));
+  const int kb0 = static_cast<int>(static_cast<long long>(g.KB) * rank / cs);
+  const int kb1 = static_cast<int>(static_cast<long long>(g.KB) * (rank + 1) / cs);
+  const int first = blockIdx.x / cs, step = gridDim.x / cs;  // (a cluster has one tile)
+  constexpr int kCols = s8_tmem_cols<BN>();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < S8_BUFS; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&mapX);
+    tma_prefetch_desc(&mapW);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kCols);
+    tmem_relinquish();
+  }
+  if (warp >= 2) {
+    for (int i = threadIdx.x - 64; i < (kb1 - kb0) * BN; i += 128) {
+      const int c = i % BN, kb = i / BN;
+      xs[i] = c < g.M ? g.sa[static_cast<size_t>(c) * g.KB + kb0 + kb] : 0.f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl wc{abort_flag, &g_fp8_status, g.wait_limit_ns};
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = first; t < g.n_tiles && ok; t += step) {
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = ring + stage * s8_stage_bytes<BN>();
+          mbar_arrive_expect_tx(&full[stage], s8_stage_bytes<BN>());
+          tma_load_2d(&mapW, &full[stage], dst, kb * 128, t * 128);
+          tma_load_2d(&mapX, &full[stage], dst + S8_W, kb * 128, 0);
+          ++issued;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      int s = stage;
+      uint32_t ph = phase;
+      for (int i = 0; i < S && i < issued; ++i) {
+        if (--s < 0) {
+          s = S - 1;
+          ph ^= 1u;
+        }
+        mbar_drain_wait(&empty[s], ph, g.wait_limit_ns);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3_f32(128, BN);
+      const uint64_t d0 = smem_desc_sw128(0, 16u, 1024u);
+      const uint32_t hi = static_cast<uint32_t>(d0 >> 32);
+      const uint32_t r0 = static_cast<uint32_t>(d0) + ((smem_u32(ring) & 0x3FFFFu) >> 4);
+      int stage = 0;
+      uint32_t phase = 0, it = 0;
+      bool ok = true;
+      for (int t = first; t < g.n_tiles && ok; t += step) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const uint32_t buf = it % S8_BUFS;
+          if (!mbar_wait(&tempty[buf], ((it / S8_BUFS) & 1) ^ 1u, wc) ||
+              !mbar_wait(&full[stage], phase, wc)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t w = r0 + stage * (s8_stage_bytes<BN>() >> 4);
+#pragma unroll
+          for (uint32_t k = 0; k < 4; ++k)
+            tc_mma_f8(tmem + buf * BN, (static_cast<uint64_t>(hi) << 32) | (w + 2 * k),
+                      (static_cast<uint64_t>(hi) << 32) | (w + (S8_W >> 4) + 2 * k), idesc, k);
+          tc_commit(&empty[stage]);
+          tc_commit(&tfull[buf]);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      tc_commit(drain);
+      mbar_drain_wait(drain, 0, g.wait_limit_ns);
+    }
+    __syncwarp();
+  }
+  bool ok = true;
+  uint64_t acc[BN / 2];
+  const int quad = warp & 3;
+  if (warp >= 2) {
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    uint32_t it = 0;
+    for (int t = first; t < g.n_tiles && ok; t += step) {
+      const float* sb = g.sb + static_cast<size_t>(t) * g.KB;
+#pragma unroll
+      for (int i = 0; i < BN / 2; ++i) acc[i] = 0;
+      float s_next = __ldg(sb + kb0);
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        const uint32_t buf = it % S8_BUFS;
+        const uint64_t s = f2_pack(s_next, s_next);
+        if (kb + 1 < kb1) s_next = __ldg(sb + kb + 1);
+        if (!mbar_wait(&tfull[buf], (it / S8_BUFS) & 1, wc)) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        const ulonglong2* x2 = reinterpret_cast<const ulonglong2*>(xs + (kb - kb0) * BN);
+        uint32_t r[2][16];
+        tmem_ld16_async(tl + buf * BN, r[0]);
+#pragma unroll
+        for (int c = 0; c < BN / 16; ++c) {
+          tmem_wait16(r[c & 1]);
+          if (c + 1 < BN / 16) {
+            tmem_ld16_async(tl + buf * BN + (c + 1) * 16, r[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[buf]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const ulonglong2 x = x2[c * 4 + i];
+            const uint32_t* q = &r[c & 1][4 * i];
+            acc[8 * c + 2 * i] =
+                f2_fma(f2_pack(__uint_as_float(q[0]), __uint_as_float(q[1])),
+                       f2_mul(x.x, s), acc[8 * c + 2 * i]);
+            acc[8 * c + 2 * i + 1] =
+                f2_fma(f2_pack(__uint_as_float(q[2]), __uint_as_float(q[3])),
+                       f2_mul(x.y, s), acc[8 * c + 2 * i + 1]);
+          }
+        }
+      }
+      if (cs == 1 && ok) {
+        const int n = t * 128 + quad * 32 + lane;
+        if (n < g.N) {
+          const float b =
+              g.bias != nullptr ? static_cast<float>(static_cast<const TO*>(g.bias)[n]) : 0.f;
+          TO* d = static_cast<TO*>(g.D) + n;
+#pragma unroll
+          for (int i = 0; i < BN / 2; ++i) {
+            const float2 p = f2_unpack(acc[i]);
+            if (2 * i < g.M) d[static_cast<size_t>(2 * i) * g.N] = fp8_out<TO>(p.x + b);
+            if (2 * i + 1 < g.M) d[static_cast<size_t>(2 * i + 1) * g.N] = fp8_out<TO>(p.y + b);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+  if (cs > 1) {
+    // the ring is free (every MMA has read it): [BN][128] sums of this part
+    float* part = reinterpret_cast<float*>(ring);
+    if (warp >= 2) {
+#pragma unroll
+      for (int i = 0; i < BN / 2; ++i) {
+        const float2 p = f2_unpack(acc[i]);
+        part[(2 * i) * 128 + quad * 32 + lane] = p.x;
+        part[(2 * i + 1) * 128 + quad * 32 + lane] = p.y;
+      }
+    }
+    cluster_sync();
+    // CTA r adds and stores tokens r, r + cs, ...
+    if (warp >= 2 && ok) {
+      const int l = quad * 32 + lane, n = first * 128 + l;
+      if (n < g.N) {
+        const float b =
+            g.bias != nullptr ? static_cast<float>(static_cast<const TO*>(g.bias)[n]) : 0.f;
+        for (int c = static_cast<int>(rank); c < g.M; c += static_cast<int>(cs)) {
+          const uint32_t at = smem_u32(part + c * 128 + l);
+          float v = 0.f;
+          for (uint32_t r = 0; r < cs; ++r) {
+            float p;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(mapa_shared(at, r)));
+            v += p;
+          }
+          static_cast<TO*>(g.D)[static_cast<size_t>(c) * g.N + n] = fp8_out<TO>(v + b);
+        }
+      }
+    }
+    cluster_sync();  // nobody leaves while its part is read
+  }
+}
+
+}  // namespace flkl

@@ -1,14 +1,21 @@
 // Host side of the scoring entry points declared in include/flkl.h: e4m3
 // quantisers, the block-scaled product, token log-probabilities.
 
+#include <algorithm>
 #include <cmath>
 #include <type_traits>
 
+#include <cudaTypedefs.h>
+
 #include "../../include/flkl.h"
+#include "fp8_gemm.cuh"
 #include "fp8_kernels.cuh"
 #include "token_logprobs.cuh"
 
 namespace flkl {
+
+extern unsigned long long g_wait_limit_ns;  // flkl_api.cu
+
 namespace {
 
 constexpr int64_t kMaxDim = int64_t(1) << 31;
@@ -32,6 +39,128 @@ flkl_status quantize(const void* src, int64_t rows, int64_t cols, int block_rows
                                                     static_cast<int>(cols),
                                                     static_cast<uint8_t*>(q), scale);
   return launched();
+}
+
+// ---------------------------------------------------------------- product
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
+}
+
+// Byte matrix [rows][K], box {128, box_rows}, 128-byte swizzle, zeros outside.
+bool fp8_map(CUtensorMap* m, const void* base, int64_t K, int64_t rows, uint32_t box_rows) {
+  const auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
+  const cuuint32_t box[2] = {128, box_rows}, estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMaxDevices = 64;
+constexpr size_t kMaxSmem = 227 * 1024;
+
+// Per device: SMs, and whether a kernel's shared memory limit has been raised.
+int device_sms() {
+  static int cache[kMaxDevices] = {};
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 148;
+  if (cache[dev] > 0) return cache[dev];
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    n = 148;
+  return cache[dev] = n;
+}
+
+template <typename K>
+bool raise_smem(K kern, bool (&done)[kMaxDevices]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  if (!done[dev])
+    done[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(kMaxSmem)) == cudaSuccess;
+  return done[dev];
+}
+
+struct Fp8Call {
+  const void *A, *B;
+  int64_t K;
+  Fp8Gemm g;
+  cudaStream_t st;
+};
+
+template <typename TO>
+flkl_status launch_pair(const Fp8Call& c) {
+  static bool done[kMaxDevices];
+  if (!raise_smem(k_fp8_pair<TO>, done)) return FLKL_ERR_CUDA;
+  Fp8Gemm g = c.g;
+  g.m_tiles = (g.M - 1) / 256 + 1;
+  g.n_tiles = (g.N - 1) / 256 + 1;
+  g.vec = (size_t(g.N) * sizeof(TO)) % 16 == 0 && aligned(g.D, 16);
+  const int64_t tiles = int64_t(g.m_tiles) * g.n_tiles;
+  if (tiles >= (int64_t(1) << 30)) return FLKL_ERR_UNSUPPORTED;
+  CUtensorMap ma, mb;
+  if (!fp8_map(&ma, c.A, c.K, g.M, 128) || !fp8_map(&mb, c.B, c.K, g.N, 128))
+    return FLKL_ERR_CUDA;
+  const int pairs = static_cast<int>(std::min<int64_t>(device_sms() / 2, tiles));
+  k_fp8_pair<TO><<<2 * pairs, P8_THREADS, P8_SMEM, c.st>>>(ma, mb, g);
+  return launched();
+}
+
+template <typename TO, int BN>
+flkl_status launch_skinny(const Fp8Call& c, int cluster) {
+  static bool done[kMaxDevices];
+  if (!raise_smem(k_fp8_skinny<TO, BN>, done)) return FLKL_ERR_CUDA;
+  Fp8Gemm g = c.g;
+  g.n_tiles = (g.N + 127) / 128;
+  const size_t fixed = s8_smem_fixed<BN>((g.KB + cluster - 1) / cluster);
+  const size_t stages = std::min<size_t>((kMaxSmem - fixed) / s8_stage_bytes<BN>(), S8_MAX_STAGES);
+  g.stages = static_cast<int>(stages);
+  CUtensorMap mx, mw;
+  if (!fp8_map(&mx, c.A, c.K, g.M, BN) || !fp8_map(&mw, c.B, c.K, g.N, 128)) return FLKL_ERR_CUDA;
+  const int ctas =
+      cluster == 1 ? std::min(device_sms(), g.n_tiles) : g.n_tiles * cluster;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(S8_THREADS);
+  cfg.dynamicSmemBytes = fixed + stages * s8_stage_bytes<BN>();
+  cfg.stream = c.st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(cluster);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_fp8_skinny<TO, BN>, mx, mw, g) == cudaSuccess ? FLKL_OK
+                                                                                 : FLKL_ERR_CUDA;
+}
+
+template <typename TO>
+flkl_status fp8_matmul(const Fp8Call& c) {
+  const int M = c.g.M, KB = c.g.KB, sms = device_sms();
+  if (M <= 128) {
+    // CTAs that share a tile of 128 weight rows: as many as leave none idle
+    const int n_tiles = (c.g.N + 127) / 128;
+    const int cluster = std::max(1, std::min({S8_MAX_CLUSTER, sms / n_tiles, KB}));
+    const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    // (the tokens' scales have to leave room for three stages and the parts)
+    if (s8_smem_fixed<128>((KB + cluster - 1) / cluster) + 4 * s8_stage_bytes<128>() <= kMaxSmem) {
+      if (bn == 16) return launch_skinny<TO, 16>(c, cluster);
+      if (bn == 32) return launch_skinny<TO, 32>(c, cluster);
+      if (bn == 64) return launch_skinny<TO, 64>(c, cluster);
+      return launch_skinny<TO, 128>(c, cluster);
+    }
+  }
+  return launch_pair<TO>(c);
 }
 
 }  // namespace
@@ -67,24 +196,34 @@ flkl_status flkl_fp8_block_matmul(const void* A, const float* a_scale, const voi
   if (!aligned(A, 16) || !aligned(B, 16) || !aligned(D, e) || !aligned(a_scale, 4) ||
       !aligned(b_scale, 4) || !aligned(bias, e))
     return FLKL_ERR_UNSUPPORTED;
-  Fp8Args a{};
-  a.A = static_cast<const uint8_t*>(A);
-  a.sa = a_scale;
-  a.B = static_cast<const uint8_t*>(B);
-  a.sb = b_scale;
-  a.bias = bias;
-  a.M = static_cast<int>(M);
-  a.N = static_cast<int>(N);
-  a.K = static_cast<int>(K);
-  a.KB = static_cast<int>((K + kScaleBlock - 1) / kScaleBlock);
-  a.D = D;
-  const int64_t mt = (M + 63) / 64;
-  if (mt > 65535) return FLKL_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>((N + 63) / 64), static_cast<unsigned>(mt));
+  Fp8Call c{};
+  c.A = A;
+  c.B = B;
+  c.K = K;
+  c.st = static_cast<cudaStream_t>(stream);
+  c.g.sa = a_scale;
+  c.g.sb = b_scale;
+  c.g.bias = bias;
+  c.g.D = D;
+  c.g.M = static_cast<int>(M);
+  c.g.N = static_cast<int>(N);
+  c.g.KB = static_cast<int>((K + kScaleBlock - 1) / kScaleBlock);
+  c.g.wait_limit_ns = g_wait_limit_ns;
+  return out_dtype == FLKL_DTYPE_BF16 ? fp8_matmul<__nv_bfloat16>(c) : fp8_matmul<float>(c);
+}
+
+flkl_status flkl_fp8_device_status(void* stream) {
+  void* p = nullptr;
+  if (cudaGetSymbolAddress(&p, g_fp8_status) != cudaSuccess) return FLKL_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (out_dtype == FLKL_DTYPE_BF16) k_fp8_simt<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
-  else k_fp8_simt<float><<<grid, 256, 0, st>>>(a);
-  return launched();
+  int h = 0;
+  if (cudaMemcpyAsync(&h, p, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
+    return FLKL_ERR_CUDA;
+  if (h != 0 && (cudaMemsetAsync(p, 0, sizeof(int), st) != cudaSuccess ||
+                 cudaStreamSynchronize(st) != cudaSuccess))
+    return FLKL_ERR_CUDA;
+  return static_cast<flkl_status>(h);
 }
 
 flkl_status flkl_token_logprobs_forward(const void* logits, int64_t row_stride,
