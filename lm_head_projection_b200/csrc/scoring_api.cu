@@ -163,6 +163,29 @@ flkl_status fp8_matmul(const Fp8Call& c) {
   return launch_pair<TO>(c);
 }
 
+// --------------------------------------------------------- log-probabilities
+template <typename T, bool TOP>
+flkl_status launch_logprobs(const LpFwdArgs& a, cudaStream_t st) {
+  // CTAs per row: a power of two up to 8 that brings two CTAs to each SM, as
+  // long as each has a tile of its own
+  int parts = 1;
+  while (parts < 8 && int64_t(a.rows) * parts * 2 <= 2 * device_sms() &&
+         a.V / (parts * 2) >= LP_NT * 16 / static_cast<int>(sizeof(T)))
+    parts *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(int64_t(a.rows) * parts));
+  cfg.blockDim = dim3(LP_NT);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(parts);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = parts > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k_token_logprobs<T, TOP>, a) == cudaSuccess ? FLKL_OK
+                                                                             : FLKL_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace flkl
 
@@ -263,16 +286,10 @@ flkl_status flkl_token_logprobs_forward(const void* logits, int64_t row_stride,
   a.top_logp = top_logp;
   a.top_ids = top_ids;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>(rows);
-  const bool bf = dtype == FLKL_DTYPE_BF16;
-  if (top_k > 0) {
-    if (bf) k_token_logprobs<__nv_bfloat16, true><<<grid, LP_NT, 0, st>>>(a);
-    else k_token_logprobs<float, true><<<grid, LP_NT, 0, st>>>(a);
-  } else {
-    if (bf) k_token_logprobs<__nv_bfloat16, false><<<grid, LP_NT, 0, st>>>(a);
-    else k_token_logprobs<float, false><<<grid, LP_NT, 0, st>>>(a);
-  }
-  return launched();
+  if (dtype == FLKL_DTYPE_BF16)
+    return top_k > 0 ? launch_logprobs<__nv_bfloat16, true>(a, st)
+                     : launch_logprobs<__nv_bfloat16, false>(a, st);
+  return top_k > 0 ? launch_logprobs<float, true>(a, st) : launch_logprobs<float, false>(a, st);
 }
 
 flkl_status flkl_token_logprobs_backward(const void* logits, int64_t row_stride,

@@ -12,14 +12,22 @@
 // scaled, so that a row of the type's lowest values stays finite, and t is cut
 // at -200, below which 2^t is 0 in fp32 (0 times -infinity would not be).
 //
-// The k best: a thread compares the largest of each of its vectors with a
-// bound that at least k of the row's logits reach; what passes is appended to
-// a list in shared memory, as a 64-bit key (ordered value, then the lower
-// index first), and the list is cut to its k best (the bound is then the k-th)
-// as it grows.  The first bound is the k-th largest of a warp's 32 lane maxima.
-// A random row appends a few hundred of its 128k logits; a tile that overflows
-// the list (a row of equal logits, or one that ascends) is appended in rounds
-// of one vector per thread, each cut before the next.
+// The k best cost the pass next to nothing: each thread's running maximum is the
+// largest of its 1/256 of the row, at least k logits reach the k-th largest of
+// those maxima, and only the threads that reach it (k, without ties) hold such
+// logits.  The few of their vectors that hold any are read again (a thread
+// leaves the maximum of every 4 vectors in shared memory), and what passes goes
+// to a list there as 64-bit keys (ordered value, then the lower index first),
+// which is cut to its k best.  Ties: where many threads reach the bound (rows of
+// equal logits, masks of one value with less than k tokens left), what is above
+// the bound is collected so and the equals are then taken from the row's
+// beginning until k are there; and a list that overflows (a row whose large
+// logits all sit in few threads' vectors) is collected in rounds over the whole
+// row, each cut before the next.
+//
+// One CTA per row; rows that are too few to fill the machine are split over a
+// cluster of 2, 4 or 8 CTAs, which leave their sums and k best in shared memory
+// for the first to join, in rank order.
 #pragma once
 
 #include "ptx.cuh"
@@ -28,9 +36,13 @@ namespace flkl {
 
 constexpr int LP_NT = 256;          // threads per CTA
 constexpr int LP_U = 4;             // 16-byte vectors per thread and tile
+constexpr int LP_CTAS = 4;          // CTAs per SM (64 registers a thread)
+constexpr int LP_TILE = LP_NT * LP_U;  // vectors per CTA and tile
 constexpr int LP_MAX_K = 32;        // alternatives at most (one per lane)
 constexpr int LP_TRIG = 64;         // appended keys above k that make a cut worth it
 constexpr int LP_CAP = LP_NT * 8 + LP_MAX_K + LP_TRIG + 32;  // keys the list holds
+constexpr int LP_MAX_REACH = 64;    // threads that reach the bound: more are ties
+constexpr int LP_SLOTS = 32;        // maxima that a thread leaves
 
 struct LpFwdArgs {
   const void* logits;
@@ -67,9 +79,11 @@ __device__ __forceinline__ float fmax_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+// (.ftz: what is below 2^-126 counts as 0; without it every call scales its
+// argument and result around the instruction)
 __device__ __forceinline__ float ex2(float t) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(t));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(t));
   return r;
 }
 
@@ -88,6 +102,29 @@ struct LpVec<__nv_bfloat16> {
     return fmax_nan(bf16lo(c), bf16hi(c));
   }
   __device__ static float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  __device__ static float max4(const uint4 (&v)[4]) {
+    uint32_t m[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint32_t a, b;
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(v[u].x), "r"(v[u].y));
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(v[u].z), "r"(v[u].w));
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m[u]) : "r"(a), "r"(b));
+    }
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m[0]) : "r"(m[0]), "r"(m[1]));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m[2]) : "r"(m[2]), "r"(m[3]));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m[0]) : "r"(m[0]), "r"(m[2]));
+    return fmax_nan(bf16lo(m[0]), bf16hi(m[0]));
+  }
+  // all 8 to at least lo (two copies of a bf16 number); NaN stays
+  __device__ static uint4 raise_to(const uint4& u, uint32_t lo) {
+    uint4 r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(u.x), "r"(lo));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(u.y), "r"(lo));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.z) : "r"(u.z), "r"(lo));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r.w) : "r"(u.w), "r"(lo));
+    return r;
+  }
 };
 template <>
 struct LpVec<float> {
@@ -101,42 +138,42 @@ struct LpVec<float> {
     return fmax_nan(fmax_nan(__uint_as_float(u.x), __uint_as_float(u.y)),
                     fmax_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
   }
+  __device__ static float max4(const uint4 (&v)[4]) {
+    return fmax_nan(fmax_nan(max(v[0]), max(v[1])), fmax_nan(max(v[2]), max(v[3])));
+  }
+  __device__ static uint4 raise_to(const uint4& u, uint32_t) { return u; }  // (not called)
   __device__ static float one(const float* p) { return *p; }
 };
 
-// Running softmax sums of one thread (base 2; c = log2(e) / T).
+// Running softmax sums (base 2; c = log2(e) / T).  A NaN logit makes m, S and A
+// NaN.
 struct LpSums {
   float m, S, A;
   __device__ void init() { m = -INFINITY; S = A = 0.f; }
-  __device__ void raise(float nm, float c) {  // nm > m
-    const float d = fmaxf((m - nm) * c, -200.f);
+  __device__ void raise(float nm, float c) {  // nm > m, or one of them NaN
+    const float d = fmax_nan((m - nm) * c, -200.f);
     const float f = ex2(d);
     A = fmaf(d, S, A) * f;
     S *= f;
-    m = nm;
+    m = fmax_nan(m, nm);
   }
-  __device__ void add(float z, float c) {  // z <= m, or NaN
+  __device__ void add(float z, float c) {  // z <= m, m above -infinity
     const float t = fmax_nan((z - m) * c, -200.f);
     const float e = ex2(t);
     S += e;
     A = fmaf(e, t, A);
   }
   __device__ void merge(float om, float oS, float oA, float c) {
-    if (om > m) raise(om, c);
+    if (!(om <= m)) raise(om, c);
     if (om > -INFINITY) {
-      const float d = fmaxf((om - m) * c, -200.f);
+      const float d = fmax_nan((om - m) * c, -200.f);
       const float f = ex2(d);
       A = fmaf(fmaf(d, oS, oA), f, A);
       S = fmaf(oS, f, S);
-    } else if (oS != oS) {
-      S = oS;  // a NaN among -infinities
     }
   }
 };
 
-__device__ __forceinline__ unsigned long long shfl_xor64(unsigned long long v, int o) {
-  return __shfl_xor_sync(0xffffffffu, v, o);
-}
 // Keys of a warp into descending order (lane 0 the largest): bitonic sort.
 template <typename K>
 __device__ __forceinline__ K warp_sort_desc(K v, int lane) {
@@ -155,12 +192,12 @@ __device__ __forceinline__ K warp_sort_desc(K v, int lane) {
 // The 32 largest of two descending lists, descending (v this lane's entry of
 // one, w_rev the other's entry 31 - lane): their elementwise maximum is
 // bitonic, five steps sort it.
-__device__ __forceinline__ unsigned long long warp_merge_desc(unsigned long long v,
-                                                              unsigned long long w_rev, int lane) {
+template <typename K>
+__device__ __forceinline__ K warp_merge_desc(K v, K w_rev, int lane) {
   v = v > w_rev ? v : w_rev;
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) {
-    const unsigned long long w = shfl_xor64(v, o);
+    const K w = __shfl_xor_sync(0xffffffffu, v, o);
     v = (lane & o) == 0 ? (v > w ? v : w) : (v > w ? w : v);
   }
   return v;
@@ -169,182 +206,309 @@ __device__ __forceinline__ unsigned long long warp_merge_desc(unsigned long long
 struct LpTopSmem {
   unsigned long long buf[LP_CAP];
   unsigned long long part[LP_NT / 32][32];
-  int cnt;
-  uint32_t bound[LP_NT / 32];
+  uint16_t slot[LP_SLOTS][LP_NT];  // the maxima's upper 16 bits (a bf16 number, cut)
+  uint16_t item[LP_MAX_REACH * LP_SLOTS];  // slot * LP_NT + thread
+  int cnt, items;
+  uint32_t bound;
 };
 
-// Cuts the list to its k best, buf[0..k) descending (0 where there are fewer).
-// Called by all threads; a barrier before it makes the appended keys visible.
-// Ends with a barrier.
-__device__ __forceinline__ void lp_cut(LpTopSmem& s, int c, int k) {
+// Cuts the list to its k best, buf[0..32) descending (0 past them).  Called by
+// all threads after a barrier that makes the keys visible; ends with one.
+__device__ __forceinline__ void lp_cut(LpTopSmem& s, int k) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = s.cnt;
+  __syncthreads();  // everyone has read the count
   unsigned long long best = 0;
   for (int b = warp * 32; b < c; b += LP_NT) {
     unsigned long long v = b + lane < c ? s.buf[b + lane] : 0ull;
     v = warp_sort_desc(v, lane);
     best = warp_merge_desc(best, __shfl_sync(0xffffffffu, v, 31 - lane), lane);
   }
-  s.part[warp][lane] = best;
-  __syncthreads();
-  // the warps' lists pairwise
-#pragma unroll
-  for (int n = LP_NT / 64; n >= 1; n >>= 1) {
-    if (warp < n) {
-      best = warp_merge_desc(best, s.part[warp + n][31 - lane], lane);
-      s.part[warp][lane] = best;
-    }
+  const int lists = min(LP_NT / 32, (c + 31) / 32);
+  if (lists > 1) {
+    s.part[warp][lane] = best;
     __syncthreads();
+    if (warp == 0)
+      for (int w = 1; w < lists; ++w) best = warp_merge_desc(best, s.part[w][31 - lane], lane);
   }
-  if (warp == 0 && lane < k) s.buf[lane] = best;
-  if (threadIdx.x == 0) s.cnt = k;
+  if (warp == 0) s.buf[lane] = lane < k ? best : 0ull;
+  if (threadIdx.x == 0) s.cnt = min(c, k);
   __syncthreads();
 }
 
+// One CTA's share of a row: 16-byte vectors [v0, v1) from zv (logit head + E v
+// on) and `extra` single logits before the first and after the last vector;
+// thread t has vectors v0 + t, v0 + t + 256, ... and single t.
+template <typename T>
+struct LpPart {
+  using VT = LpVec<T>;
+  const T* z;
+  const uint4* zv;
+  int v0, v1, head, tail0, own_head, extra;
+  // tiles (of LP_TILE vectors) per slot: 2^this
+  __device__ int slot_shift() const {
+    int sh = 0;
+    while ((v1 - v0 - 1) / LP_TILE >> sh >= LP_SLOTS) ++sh;
+    return sh;
+  }
+  __device__ int extra_index(int i) const { return i < own_head ? i : tail0 + i - own_head; }
+
+  __device__ void append(LpTopSmem& s, float f, int idx) const {
+    const int p = atomicAdd(&s.cnt, 1);
+    if (p < LP_CAP) s.buf[p] = lp_key(f, static_cast<uint32_t>(idx));
+  }
+  // Logits of vector i from order value lo on (with `only`: of just that value).
+  __device__ void append_vec(LpTopSmem& s, int i, uint32_t lo, bool only) const {
+    append_raw(s, ld_nc_v4(zv + i), i, lo, only);
+  }
+  __device__ void append_raw(LpTopSmem& s, const uint4& raw, int i, uint32_t lo,
+                             bool only) const {
+    if (lp_ord(VT::max(raw)) < lo) return;
+    float f[VT::E];
+    VT::unpack(raw, f);
+#pragma unroll
+    for (int j = 0; j < VT::E; ++j) {
+      const uint32_t o = lp_ord(f[j]);
+      if (only ? o == lo : o >= lo) append(s, f[j], head + i * VT::E + j);
+    }
+  }
+  __device__ void append_one(LpTopSmem& s, int i, uint32_t lo, bool only) const {
+    const int idx = extra_index(i);
+    const float f = VT::one(z + idx);
+    const uint32_t o = lp_ord(f);
+    if (only ? o == lo : o >= lo) append(s, f, idx);
+  }
+
+  // All logits from order value lo on that threads with own >= lo hold, into
+  // the empty list; returns their number (which may exceed the list).
+  __device__ int collect(LpTopSmem& s, uint32_t own, uint32_t lo) const {
+    const int tid = threadIdx.x;
+    const int sh = slot_shift(), tiles = (v1 - v0 + LP_TILE - 1) / LP_TILE;
+    // (cutting keeps the order, so that no slot that holds such a logit is missed)
+    const uint32_t lo16 =
+        lo == 0 ? 0u : lp_ord(__uint_as_float(__float_as_uint(lp_unord(lo)) & 0xFFFF0000u));
+    if (own >= lo && own > 0) {
+      for (int q = 0; q << sh < tiles; ++q)
+        if (lp_ord(__uint_as_float(static_cast<uint32_t>(s.slot[q][tid]) << 16)) >= lo16)
+          s.item[atomicAdd(&s.items, 1)] = static_cast<uint16_t>(q * LP_NT + tid);
+      if (tid < extra) append_one(s, tid, lo, false);
+    }
+    __syncthreads();
+    // the vectors of those slots, one per thread whoever's they were
+    const int per = LP_U << sh, n = s.items * per;
+    for (int w = tid; w < n; w += LP_NT) {
+      const int it = s.item[w / per], u = w % per;
+      const int i = v0 + (it / LP_NT << sh) * LP_TILE + u * LP_NT + it % LP_NT;
+      if (i < v1) append_vec(s, i, lo, false);
+    }
+    __syncthreads();
+    return s.cnt;
+  }
+  // The k best (or all) from order value lo on, in rounds over the whole part in
+  // index order: what ties with the k-th of a cut list comes later and loses.
+  __device__ void rounds(LpTopSmem& s, uint32_t lo, int k) const {
+    const int tid = threadIdx.x;
+    __syncthreads();  // everyone has read the count
+    if (tid == 0) s.cnt = 0;
+    __syncthreads();
+    if (tid < own_head) append_one(s, tid, lo, false);
+    for (int b = v0; b < v1 || b == v0; b += LP_NT) {
+      if (b + tid < v1) append_vec(s, b + tid, lo, false);
+      if (b + LP_NT >= v1 && tid >= own_head && tid < extra) append_one(s, tid, lo, false);
+      __syncthreads();
+      const int n = s.cnt;
+      __syncthreads();
+      if (n > k + LP_TRIG) {
+        lp_cut(s, k);
+        const uint32_t o = static_cast<uint32_t>(s.buf[k - 1] >> 32);
+        __syncthreads();
+        if (o == 0xFFFFFFFFu) return;
+        lo = o + 1;
+      }
+    }
+    lp_cut(s, k);
+  }
+  // Logits of order value `eq`, in index order, until the list holds k.
+  __device__ void equals(LpTopSmem& s, uint32_t eq, int k) const {
+    const int tid = threadIdx.x;
+    if (tid < own_head) append_one(s, tid, eq, true);
+    for (int b = v0; b < v1 || b == v0; b += LP_NT) {
+      if (b + tid < v1) append_vec(s, b + tid, eq, true);
+      if (b + LP_NT >= v1 && tid >= own_head && tid < extra) append_one(s, tid, eq, true);
+      __syncthreads();
+      const int n = s.cnt;
+      __syncthreads();
+      if (n >= k) return;
+    }
+  }
+  // buf[0..32): the part's k best, descending.  `own` is the order value of the
+  // thread's largest logit (0: it has none).
+  __device__ void top(LpTopSmem& s, uint32_t own, int k) const {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // the k-th largest of the threads' largest: each warp's in order, then the
+    // 8 lists merged in pairs
+    uint32_t best = warp_sort_desc(own, lane);
+    uint32_t(*part)[32] = reinterpret_cast<uint32_t(*)[32]>(s.part);
+    part[warp][lane] = best;
+    if (tid == 0) s.cnt = s.items = 0;
+    __syncthreads();
+#pragma unroll
+    for (int n = LP_NT / 64; n >= 1; n >>= 1) {
+      if (warp < n) {
+        best = warp_merge_desc(best, part[warp + n][31 - lane], lane);
+        part[warp][lane] = best;
+        if (n == 1 && lane == k - 1) s.bound = best;
+      }
+      __syncthreads();
+    }
+    const uint32_t lo = s.bound;
+    const int reach = __syncthreads_count(own >= lo && own > 0);
+    if (reach <= LP_MAX_REACH || lo == 0) {
+      const int n = collect(s, own, lo);
+      if (n <= LP_CAP) lp_cut(s, k);
+      else rounds(s, lo, k);
+      return;
+    }
+    const int n = lo == 0xFFFFFFFFu ? 0 : collect(s, own, lo + 1);
+    if (n > LP_CAP) {
+      rounds(s, lo + 1, k);
+      return;
+    }
+    __syncthreads();  // everyone has read the count
+    if (n < k) equals(s, lo, k);
+    lp_cut(s, k);
+  }
+};
+
+struct LpShared {
+  float3 red[LP_NT / 32];
+  float3 sums;  // the CTA's, read by the cluster's first
+};
+
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(LP_NT) k_token_logprobs(const LpFwdArgs a) {
+__global__ void __launch_bounds__(LP_NT, LP_CTAS) k_token_logprobs(const LpFwdArgs a) {
   using VT = LpVec<T>;
   constexpr int E = VT::E;
-  __shared__ float3 red[LP_NT / 32];
+  __shared__ LpShared sh;
   __shared__ typename std::conditional<TOP, LpTopSmem, int>::type top_mem;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = blockIdx.x;
+  uint32_t parts;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(parts));
+  const uint32_t rank = cluster_cta_rank();
+  const int row = blockIdx.x / parts;
   const long long y = a.target != nullptr ? a.target[row] : -1;
-  if (a.target != nullptr && y == a.ignore_index) {  // the whole CTA
-    if (tid == 0) {
-      a.logp[row] = 0.f;
-      a.entropy[row] = 0.f;
-      a.lse[row] = 0.f;
-      a.stats[row] = make_float2(-INFINITY, 0.f);
-    }
-    if (TOP && tid < a.k) {
-      a.top_logp[static_cast<size_t>(row) * a.k + tid] = 0.f;
-      a.top_ids[static_cast<size_t>(row) * a.k + tid] = -1;
+  if (a.target != nullptr && y == a.ignore_index) {  // the whole cluster
+    if (rank == 0) {
+      if (tid == 0) {
+        a.logp[row] = 0.f;
+        a.entropy[row] = 0.f;
+        a.lse[row] = 0.f;
+        a.stats[row] = make_float2(-INFINITY, 0.f);
+      }
+      if (TOP && tid < a.k) {
+        a.top_logp[static_cast<size_t>(row) * a.k + tid] = 0.f;
+        a.top_ids[static_cast<size_t>(row) * a.k + tid] = -1;
+      }
     }
     return;
   }
-  const T* z = static_cast<const T*>(a.logits) + static_cast<long long>(row) * a.ld;
+  LpPart<T> p;
+  p.z = static_cast<const T*>(a.logits) + static_cast<long long>(row) * a.ld;
+  const float zy = y >= 0 && y < a.V ? VT::one(p.z + y) : 0.f;
   const float c = 1.4426950408889634f / a.temperature;
   // the row as [head][vectors of 16 aligned bytes][tail]
-  const int head = min(a.V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(z) & 15)) & 15) /
-                                static_cast<int>(sizeof(T)));
-  const int nvec = (a.V - head) / E;
-  const int tail0 = head + nvec * E;
-  const uint4* zv = reinterpret_cast<const uint4*>(z + head);
+  p.head = min(a.V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p.z) & 15)) & 15) /
+                        static_cast<int>(sizeof(T)));
+  const int nvec = (a.V - p.head) / E;
+  p.tail0 = p.head + nvec * E;
+  p.zv = reinterpret_cast<const uint4*>(p.z + p.head);
+  p.v0 = static_cast<int>(static_cast<long long>(nvec) * rank / parts);
+  p.v1 = static_cast<int>(static_cast<long long>(nvec) * (rank + 1) / parts);
+  p.own_head = rank == 0 ? p.head : 0;
+  p.extra = p.own_head + (rank == parts - 1 ? a.V - p.tail0 : 0);
 
   LpSums sum;
   sum.init();
-  float bound = -INFINITY;      // what a vector's largest has to reach to be looked at
-  uint32_t bound_ord = 0;       // keys from here on are appended
-  int count = 0;                // keys in the list when the tile begins (uniform)
-  if constexpr (TOP) {
-    if (tid == 0) top_mem.cnt = 0;
+  // bf16: what lies 200 powers of two below the maximum has 2^t = 0, so logits
+  // are first raised to there, two at a time, where that is a finite number
+  // (`near`): then no t is -infinity and needs a look of its own.
+  const float reach = 200.f / c;
+  bool near = false;
+  uint32_t lo2 = 0;
+  auto new_max = [&](float m) {
+    sum.raise(m, c);
+    if constexpr (E == 8) {
+      const float l = m - reach;
+      near = l > -3.3e38f && m < 3e38f;
+      // a bf16 number below l, and so below m even where m - reach rounds to m
+      lo2 = __bfloat16_as_ushort(__float2bfloat16_rd(l - fabsf(l) * 0x1p-8f)) * 0x10001u;
+    }
+  };
+  if (tid < p.extra) {  // at most 2 (E - 1) single logits
+    const float x = VT::one(p.z + p.extra_index(tid));
+    if (!(x <= sum.m)) new_max(x);
+    if (sum.m > -INFINITY) sum.add(x, c);
   }
-  // head and tail: at most 2 (E - 1) logits, one per thread
-  const int extra = head + (a.V - tail0);
-  float xz = -INFINITY;
-  int xi = -1;
-  if (tid < extra) {
-    xi = tid < head ? tid : tail0 + tid - head;
-    xz = VT::one(z + xi);
-    if (xz > sum.m) sum.raise(xz, c);
-    if (sum.m > -INFINITY) sum.add(xz, c);
-    else if (xz != xz) sum.S = xz;
-  }
-
-  for (int t0 = 0; t0 < nvec || t0 == 0; t0 += LP_NT * LP_U) {
+  uint4 next[LP_U];  // the tile after the one at work, on its way
+  auto fetch = [&](int b) {
+#pragma unroll
+    for (int u = 0; u < LP_U; ++u) {
+      const int i = b + u * LP_NT + tid;
+      next[u] = i < p.v1 ? ld_nc_v4(p.zv + i) : VT::empty();
+    }
+  };
+  fetch(p.v0);
+  const int shift = TOP ? p.slot_shift() : 0;
+  int tile = 0;
+  float slot_max = -INFINITY;
+  for (int b = p.v0; b < p.v1; b += LP_TILE) {
     uint4 raw[LP_U];
 #pragma unroll
-    for (int u = 0; u < LP_U; ++u) {
-      const int i = t0 + u * LP_NT + tid;
-      raw[u] = i < nvec ? ld_nc_v4(zv + i) : VT::empty();
+    for (int u = 0; u < LP_U; ++u) raw[u] = next[u];
+    fetch(b + LP_TILE);
+    const float tm = VT::max4(raw);
+    if constexpr (TOP) {
+      slot_max = fmax_nan(slot_max, tm);
+      top_mem.slot[tile >> shift][tid] =
+          static_cast<uint16_t>(__float_as_uint(slot_max) >> 16);
+      ++tile;
+      if ((tile >> shift) << shift == tile) slot_max = -INFINITY;
     }
-    float vm[LP_U], tm = -INFINITY;
-#pragma unroll
-    for (int u = 0; u < LP_U; ++u) {
-      vm[u] = VT::max(raw[u]);
-      tm = fmax_nan(tm, vm[u]);
-    }
-    if (tm > sum.m) sum.raise(tm, c);
-    if (tm != tm) sum.S = tm;
-    if (sum.m > -INFINITY) {
+    if (!(tm <= sum.m)) new_max(tm);
+    if (E == 8 && near) {
+      // two logits an instruction, in two sums that are joined per tile
+      const uint64_t nm = f2_pack(-sum.m, -sum.m), c2 = f2_pack(c, c);
+      uint64_t S2 = f2_pack(sum.S, 0.f), A2 = f2_pack(sum.A, 0.f);
 #pragma unroll
       for (int u = 0; u < LP_U; ++u) {
+        float f[E];
+        VT::unpack(VT::raise_to(raw[u], lo2), f);
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+          const uint64_t t = f2_mul(f2_add(f2_pack(f[i], f[i + 1]), nm), c2);
+          const float2 t2 = f2_unpack(t);
+          const uint64_t e = f2_pack(ex2(t2.x), ex2(t2.y));
+          S2 = f2_add(S2, e);
+          A2 = f2_fma(e, t, A2);
+        }
+      }
+      const float2 Sp = f2_unpack(S2), Ap = f2_unpack(A2);
+      sum.S = Sp.x + Sp.y;
+      sum.A = Ap.x + Ap.y;
+    } else if (sum.m > -INFINITY) {
+#pragma unroll
+      for (int u = 0; u < LP_U; ++u) {
+        if (b + u * LP_NT + warp * 32 >= p.v1) break;
         float f[E];
         VT::unpack(raw[u], f);
 #pragma unroll
         for (int i = 0; i < E; ++i) sum.add(f[i], c);
       }
     }
-    if constexpr (TOP) {
-      const bool first = t0 == 0;
-      if (first) {
-        // a bound that at least k logits of the tile reach
-        uint32_t o = warp_sort_desc(lp_ord(tm), lane);
-        o = __shfl_sync(0xffffffffu, o, a.k - 1);
-        if (lane == 0) top_mem.bound[warp] = o;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < LP_NT / 32; ++w) bound_ord = max(bound_ord, top_mem.bound[w]);
-        bound = bound_ord == 0xFFFFFFFFu ? INFINITY : lp_unord(bound_ord);
-      }
-      auto append = [&](float f, int idx) {
-        if (lp_ord(f) < bound_ord) return false;
-        const int p = atomicAdd(&top_mem.cnt, 1);
-        if (p < LP_CAP) top_mem.buf[p] = lp_key(f, static_cast<uint32_t>(idx));
-        return true;
-      };
-      auto append_vec = [&](int u) {
-        const int i0 = t0 + u * LP_NT + tid;
-        bool any = false;
-        if (!(vm[u] < bound) && i0 < nvec) {
-          float f[E];
-          VT::unpack(raw[u], f);
-#pragma unroll
-          for (int i = 0; i < E; ++i) any |= append(f[i], head + i0 * E + i);
-        }
-        return any;
-      };
-      // after the list is cut: the bound is its k-th key, later equals lose
-      auto lower = [&]() {
-        const unsigned long long kth = top_mem.buf[a.k - 1];
-        if (kth != 0) {
-          const uint32_t o = static_cast<uint32_t>(kth >> 32);
-          bound = o == 0xFFFFFFFFu ? INFINITY : lp_unord(o);
-          bound_ord = o == 0xFFFFFFFFu ? o : o + 1;
-        }
-      };
-      bool any = false;
-#pragma unroll
-      for (int u = 0; u < LP_U; ++u) any |= append_vec(u);
-      if (first && xi >= 0) any |= append(xz, xi);
-      if (__syncthreads_or(any)) {
-        int n = top_mem.cnt;
-        __syncthreads();
-        if (n > LP_CAP) {
-          // too many for the list: one vector per thread at a time
-          if (tid == 0) top_mem.cnt = count;
-          __syncthreads();
-          for (int u = 0; u < LP_U; ++u) {
-            append_vec(u);
-            if (u == 0 && first && xi >= 0) append(xz, xi);
-            __syncthreads();
-            n = top_mem.cnt;
-            __syncthreads();
-            lp_cut(top_mem, n, a.k);
-            lower();
-            __syncthreads();
-          }
-          count = a.k;
-        } else if (first || n > a.k + LP_TRIG) {
-          lp_cut(top_mem, n, a.k);
-          lower();
-          __syncthreads();
-          count = a.k;
-        } else {
-          count = n;
-        }
-      }
-    }
+  }
+  if constexpr (TOP) {
+    const bool any = p.v0 + tid < p.v1 || tid < p.extra;
+    p.top(top_mem, any ? lp_ord(sum.m) : 0u, a.k);
   }
 
   // sums of the CTA, warps in order
@@ -355,15 +519,40 @@ __global__ void __launch_bounds__(LP_NT) k_token_logprobs(const LpFwdArgs a) {
     const float oA = __shfl_xor_sync(0xffffffffu, sum.A, o);
     sum.merge(om, oS, oA, c);
   }
-  if (lane == 0) red[warp] = make_float3(sum.m, sum.S, sum.A);
+  if (lane == 0) sh.red[warp] = make_float3(sum.m, sum.S, sum.A);
   __syncthreads();
-  if constexpr (TOP) lp_cut(top_mem, top_mem.cnt, a.k);
-  if (warp != 0) return;
-  sum.init();
+  unsigned long long best = 0;
+  if (warp == 0) {
+    sum.init();
 #pragma unroll
-  for (int w = 0; w < LP_NT / 32; ++w) sum.merge(red[w].x, red[w].y, red[w].z, c);
+    for (int w = 0; w < LP_NT / 32; ++w) sum.merge(sh.red[w].x, sh.red[w].y, sh.red[w].z, c);
+    if constexpr (TOP) best = top_mem.buf[lane];
+  }
+  if (parts > 1) {
+    if (tid == 0) sh.sums = make_float3(sum.m, sum.S, sum.A);
+    cluster_sync();
+    if (rank == 0 && warp == 0) {
+      for (uint32_t r = 1; r < parts; ++r) {
+        const uint32_t at = mapa_shared(smem_u32(&sh.sums), r);
+        float om, oS, oA;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(om) : "r"(at));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(oS) : "r"(at + 4));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(oA) : "r"(at + 8));
+        sum.merge(om, oS, oA, c);
+        if constexpr (TOP) {
+          unsigned long long v;
+          asm volatile("ld.shared::cluster.u64 %0, [%1];"
+                       : "=l"(v)
+                       : "r"(mapa_shared(smem_u32(&top_mem.buf[31 - lane]), r)));
+          best = warp_merge_desc(best, v, lane);
+        }
+      }
+    }
+    cluster_sync();  // nobody leaves while its part is read
+  }
+  if (rank != 0 || warp != 0) return;
   // a row that holds no token: logp -inf, entropy 0
-  const bool none = sum.m == -INFINITY && sum.S == 0.f;
+  const bool none = sum.m == -INFINITY;
   const float lnS = none ? 0.f : logf(sum.S);
   if (lane == 0) {
     a.stats[row] = make_float2(sum.m, lnS);
@@ -371,18 +560,17 @@ __global__ void __launch_bounds__(LP_NT) k_token_logprobs(const LpFwdArgs a) {
     a.lse[row] = none ? -INFINITY : sum.m / a.temperature + lnS;
     if (a.logp != nullptr) {
       float lp = 0.f;
-      if (y >= 0 && y < a.V)
-        lp = none ? -INFINITY : (VT::one(z + y) - sum.m) / a.temperature - lnS;
+      if (y >= 0 && y < a.V) lp = none ? -INFINITY : (zy - sum.m) / a.temperature - lnS;
       a.logp[row] = lp;
     }
   }
   if constexpr (TOP) {
     if (lane < a.k) {
-      const unsigned long long key = top_mem.buf[lane];
-      const uint32_t idx = 0xFFFFFFFFu - static_cast<uint32_t>(key);
       const size_t o = static_cast<size_t>(row) * a.k + lane;
-      a.top_ids[o] = idx;
-      a.top_logp[o] = none ? -INFINITY : (VT::one(z + idx) - sum.m) / a.temperature - lnS;
+      a.top_ids[o] = 0xFFFFFFFFu - static_cast<uint32_t>(best);
+      a.top_logp[o] =
+          none ? -INFINITY
+               : (lp_unord(static_cast<uint32_t>(best >> 32)) - sum.m) / a.temperature - lnS;
     }
   }
 }

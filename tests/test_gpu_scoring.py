@@ -395,6 +395,50 @@ def test_logprobs_orders_that_fill_the_list(dtype, V):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows", [1, 37, 74, 75, 149, 297])
+def test_logprobs_rows_split_over_clusters(dtype, rows):
+    """8, 4, 2 and 1 CTAs per row: random rows, ties across the parts' borders,
+    largest logits at the row's ends."""
+    V = 33003
+    z, t = _logits(rows, V, dtype, 9)
+    z = z.clone()
+    z[0, ::4000] = 20.0
+    z[-1, -1] = 30.0
+    z[-1, 0] = 30.0
+    z[rows // 2, 5:] = 1.0
+    _check_logprobs(z, t, 20, grads=rows == 37)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows", [2, 300])
+def test_logprobs_few_tokens_left_by_a_mask(dtype, rows):
+    """Fewer tokens left than alternatives asked for: the masked ones follow in
+    index order."""
+    for low in (-float("inf"), torch.finfo(DT[dtype]).min):
+        z = torch.full((rows, 20003), low)
+        z[:, 20001] = 2.0
+        z[:, 19000] = 2.0
+        z[:, 77] = -1.0
+        z[0, 77] = low
+        t = torch.full((rows,), 77)
+        _check_logprobs(z.to(DT[dtype]).cuda(), t.cuda(), 20, grads=rows == 2)
+        _check_logprobs(z.to(DT[dtype]).cuda(), t.cuda(), 1, grads=False)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_logprobs_large_logits_of_few_threads(dtype):
+    """What passes the bound sits in few threads' parts and overflows the list."""
+    rows, V = 300, 128256
+    e = 4 if dtype == "fp32" else 8
+    z, t = _logits(rows, V, dtype, 10)
+    v = torch.arange(V, device="cuda") // e % 256
+    z[:, v < 20] += 40.0
+    z[1, v < 20] = 33.0
+    _check_logprobs(z, t, 32, grads=False)
+    _check_logprobs(z, t, 2, grads=False)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_logprobs_non_finite_rows(dtype):
     z, t = _logits(5, 5000, dtype, 2)
     z = z.clone()
