@@ -481,8 +481,10 @@ def _launch(what: str, call, args, dev, stream: Optional[torch.cuda.Stream]) -> 
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _launch(what, call, args, dev, stream)
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
-    status = call(*args, st.cuda_stream)
+    # (the raw handle: a Stream object costs as much as a small launch)
+    st = stream.cuda_stream if stream is not None \
+        else torch._C._cuda_getCurrentRawStream(dev.index)
+    status = call(*args, st)
     if status != FLKL_OK:
         raise FlklError(status, what)
 

@@ -19,6 +19,14 @@ constexpr int kScaleBlock = 128;  // columns (and, for weights, rows) that share
 __device__ __forceinline__ float e4m3_scale(float amax) {
   return amax < 0x1p-100f ? 1.f : amax / kE4m3Max;
 }
+// 1 / scale for the codes, within 3 of its last places (a true division per
+// block costs more than the rest of a block's arithmetic; a code moves only
+// where a value lies that close to the middle of two).
+__device__ __forceinline__ float e4m3_inv_scale(float amax) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(amax * (1.f / kE4m3Max)));
+  return amax < 0x1p-100f ? 1.f : r;
+}
 
 // 8 values times inv -> 8 codes (out-of-range values saturate, NaN stays NaN).
 __device__ __forceinline__ uint2 e4m3_pack8(const float (&v)[8], float inv) {

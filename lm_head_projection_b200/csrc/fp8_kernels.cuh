@@ -19,10 +19,10 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const T* __restrict__ src
   const bool ok = row < rows && c < cols;
   float v[8] = {};
   if (ok) Vec8<T>::load(src + row * cols + c, v);
-  const float s = e4m3_scale(half_warp_max(amax8(v)));
+  const float m = half_warp_max(amax8(v));
   if (!ok) return;
-  *reinterpret_cast<uint2*>(q + row * cols + c) = e4m3_pack8(v, 1.f / s);
-  if (l == 0) scale[row * kb + b] = s;
+  *reinterpret_cast<uint2*>(q + row * cols + c) = e4m3_pack8(v, e4m3_inv_scale(m));
+  if (l == 0) scale[row * kb + b] = e4m3_scale(m);
 }
 
 // One scale per 128 x 128 block: a CTA per block, held in registers between
@@ -52,12 +52,12 @@ __global__ void __launch_bounds__(256) k_quantize_blocks(const T* __restrict__ s
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = fmaxf(m, red[i]);
-  const float s = e4m3_scale(m);
+  const float inv = e4m3_inv_scale(m);
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (r0 + 16 * i < rows && c < cols)
-      *reinterpret_cast<uint2*>(q + (r0 + 16 * i) * cols + c) = e4m3_pack8(v[i], 1.f / s);
-  if (threadIdx.x == 0) scale[blockIdx.x] = s;
+      *reinterpret_cast<uint2*>(q + (r0 + 16 * i) * cols + c) = e4m3_pack8(v[i], inv);
+  if (threadIdx.x == 0) scale[blockIdx.x] = e4m3_scale(m);
 }
 
 }  // namespace flkl

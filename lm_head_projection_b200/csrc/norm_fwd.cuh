@@ -92,12 +92,12 @@ __global__ void __launch_bounds__(NT) k_add_rms_norm(const NormFwdArgs a) {
     }
     if constexpr (QUANT) {
       // columns [128 j, 128 j + 128) are one half warp's (G is a multiple of 32)
-      const float s = e4m3_scale(half_warp_max(amax8(h[v])));
+      const float m = half_warp_max(amax8(h[v]));
       if (c < H) {
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.Y) + off + c) =
-            e4m3_pack8(h[v], 1.f / s);
+            e4m3_pack8(h[v], e4m3_inv_scale(m));
         if ((lane & 15) == 0)
-          a.scale[static_cast<size_t>(row) * ((H + 127) / 128) + c / 128] = s;
+          a.scale[static_cast<size_t>(row) * ((H + 127) / 128) + c / 128] = e4m3_scale(m);
       }
     } else {
       if (c < H) Vec8<T>::store(static_cast<T*>(a.Y) + off + c, h[v]);
@@ -117,7 +117,7 @@ template <typename T>
 cudaError_t launch_norm_fwd(const NormFwdArgs& a, bool quant, cudaStream_t st) {
   if (a.H <= 256) return launch_norm_fwd_w<T, 128, 32, 1>(a, quant, st);
   if (a.H <= 1024) return launch_norm_fwd_w<T, 128, 128, 1>(a, quant, st);
-  if (a.H <= 2048) return launch_norm_fwd_w<T, 256, 256, 1>(a, quant, st);
+  if (a.H <= 2048) return launch_norm_fwd_w<T, 128, 128, 2>(a, quant, st);
   if (a.H <= 4096) return launch_norm_fwd_w<T, 256, 256, 2>(a, quant, st);
   return launch_norm_fwd_w<T, 512, 512, 2>(a, quant, st);
 }

@@ -29,10 +29,10 @@ def _quantize(x: torch.Tensor, block_rows: int, stream) -> Tuple[torch.Tensor, t
     _check_dev("x", x, x.dtype, x.shape, x.device)
     K = x.shape[-1]
     rows = x.numel() // K if K else 0
-    q = torch.empty(x.shape, dtype=_F8, device=x.device)
+    q = torch.empty_like(x, dtype=_F8)
     kb = -(-K // 128)
     shape = (*x.shape[:-1], kb) if block_rows == 1 else (-(-rows // 128), kb)
-    scale = torch.empty(shape, dtype=torch.float32, device=x.device)
+    scale = x.new_empty(shape, dtype=torch.float32)
     _launch("flkl_fp8_quantize", flkl_fp8_quantize,
             (x.data_ptr(), rows, K, DTYPES[x.dtype], block_rows, q.data_ptr(), scale.data_ptr()),
             x.device, stream)
@@ -76,7 +76,7 @@ def block_matmul(A: torch.Tensor, a_scale: torch.Tensor, B: torch.Tensor, b_scal
     if bias is not None:
         _check_dev("bias", bias, out_dtype, (N,), dev)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = A.new_empty((M, N), dtype=out_dtype)
     else:
         _check_dev("out", out, out_dtype, (M, N), dev)
     _launch("flkl_fp8_block_matmul", flkl_fp8_block_matmul,

@@ -56,13 +56,12 @@ def token_logprobs_forward(logits: torch.Tensor, target: Optional[torch.Tensor] 
     rows, V, ld = _check_logits(logits, target)
     if not 0 <= top_k <= min(MAX_TOP_K, V):
         raise ValueError(f"top_k must lie in [0, {min(MAX_TOP_K, V)}], got {top_k}")
-    dev = logits.device
-    f = torch.empty((5, rows), dtype=torch.float32, device=dev)
-    logp = f[4] if target is not None else None
-    stats = f[:2].view(rows, 2)
-    top_logp = torch.empty((rows, top_k), dtype=torch.float32, device=dev) if top_k else None
-    top_ids = torch.empty((rows, top_k), dtype=torch.int64, device=dev) if top_k else None
-    entropy, lse = f[2], f[3]
+    dev, f32 = logits.device, torch.float32
+    new = logits.new_empty  # (cheaper than torch.empty)
+    entropy, lse, stats = new(rows, dtype=f32), new(rows, dtype=f32), new((rows, 2), dtype=f32)
+    logp = new(rows, dtype=f32) if target is not None else None
+    top_logp = new((rows, top_k), dtype=f32) if top_k else None
+    top_ids = new((rows, top_k), dtype=torch.int64) if top_k else None
     _launch("flkl_token_logprobs_forward", flkl_token_logprobs_forward,
             (logits.data_ptr(), ld, _ptr(target), ignore_index, rows, V, DTYPES[logits.dtype],
              temperature, top_k, _ptr(logp), entropy.data_ptr(), lse.data_ptr(),
@@ -99,7 +98,7 @@ def token_logprobs_backward(logits: torch.Tensor, target: Optional[torch.Tensor]
         if not k:
             raise ValueError("dtop_logp needs alternatives (top_k > 0)")
         _check_dev("dtop_logp", dtop_logp, f32, (rows, k), dev)
-    dlogits = torch.empty_strided((rows, V), (ld, 1), dtype=logits.dtype, device=dev)
+    dlogits = logits.new_empty_strided((rows, V), (ld, 1))
     _launch("flkl_token_logprobs_backward", flkl_token_logprobs_backward,
             (logits.data_ptr(), ld, _ptr(target), ignore_index, rows, V, DTYPES[logits.dtype],
              temperature, k, stats.data_ptr(), entropy.data_ptr(), _ptr(top_ids), _ptr(dlogp),

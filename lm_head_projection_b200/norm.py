@@ -112,9 +112,8 @@ def add_rms_norm(X: torch.Tensor, W: torch.Tensor, residual: Optional[torch.Tens
         Hs = residual.detach() if inplace else torch.empty_like(X)
     elif inplace:
         raise ValueError("inplace needs a residual")
-    Y = torch.empty(X.shape, dtype=torch.float8_e4m3fn if quantize else dt, device=dev)
-    scale = torch.empty((*X.shape[:-1], -(-H // 128)), dtype=torch.float32, device=dev) \
-        if quantize else None
+    Y = torch.empty_like(X, dtype=torch.float8_e4m3fn if quantize else dt)
+    scale = X.new_empty((*X.shape[:-1], -(-H // 128)), dtype=torch.float32) if quantize else None
     _launch("flkl_add_rms_norm_forward", flkl_add_rms_norm_forward,
             (X.data_ptr(), _ptr(residual), W.data_ptr(), rows, H, DTYPES[dt], eps,
              int(bool(quantize)), Y.data_ptr(), _ptr(scale), _ptr(Hs)), dev, stream)
@@ -132,10 +131,10 @@ def add_rms_norm_backward(dY: torch.Tensor, H: torch.Tensor, W: torch.Tensor,
     if dH is not None:
         _check_dev("dH", dH, dt, H.shape, dev)
     dX = torch.empty_like(H)
-    dW = torch.empty((hidden,), dtype=pdt, device=dev) if compute_dW else None
+    dW = H.new_empty(hidden, dtype=pdt) if compute_dW else None
     with torch.cuda.device(dev):  # the size goes by the current device
         need = flkl_norm_workspace_size(rows, hidden, compute_dW, False)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    ws = H.new_empty(need, dtype=torch.uint8) if need else None
     _launch("flkl_add_rms_norm_backward", flkl_add_rms_norm_backward,
             (_ptr(dY), _ptr(dH), _ptr(H), _ptr(W), rows, hidden, DTYPES[dt], eps, compute_dW,
              accum_fp32, _ptr(dX), _ptr(dW), _ptr(ws), need), dev, stream)
