@@ -225,8 +225,18 @@ flkl_status norm_backward(int kind, const void* dY, const void* dH, const void* 
     const float* p0 = compute_dW ? a.part_w : a.part_b;
     void* o0 = compute_dW ? dW : db;
     const dim3 grid(static_cast<unsigned>((H + 31) / 32), static_cast<unsigned>(n_grads));
-    k_colsum<<<grid, kColsumThreads, 0, st>>>(p0, a.part_b, n_ctas, a.H, o0, db, out_fp32);
-    if (cudaGetLastError() != cudaSuccess) return FLKL_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kColsumThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = n_ctas > 0 ? 1 : 0;  // (without rows nothing of this call precedes it)
+    if (cudaLaunchKernelEx(&cfg, k_colsum, p0, static_cast<const float*>(a.part_b), n_ctas, a.H,
+                           o0, db, out_fp32) != cudaSuccess)
+      return FLKL_ERR_CUDA;
   }
   return FLKL_OK;
 }

@@ -297,6 +297,9 @@ __global__ void __launch_bounds__(kColsumThreads)
   void* out = blockIdx.y ? out1 : out0;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  // (launched before the partial rows are complete, so that the two kernels
+  // follow one another without a gap: waits for them here)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // 16 loads in flight per thread, then added in order (a missing row adds 0)
   constexpr int U = 16;
   float s = 0.f;

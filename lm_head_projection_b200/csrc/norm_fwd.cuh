@@ -33,7 +33,7 @@ struct NormFwdArgs {
 // G threads per row, VPT vectors of 8 columns per thread (H <= 8 G VPT);
 // NT threads per CTA, NT / G rows.
 template <typename T, int NT, int G, int VPT, bool QUANT>
-__global__ void __launch_bounds__(NT) k_add_rms_norm(const NormFwdArgs a) {
+__global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 2048 / NT : 1) k_add_rms_norm(const NormFwdArgs a) {
   constexpr int NW = G / 32;
   __shared__ float red[NW > 1 ? NW : 1];
   const int lane = threadIdx.x & 31;
