@@ -54,88 +54,129 @@ __device__ __forceinline__ __nv_bfloat16 fp8_out<__nv_bfloat16>(float v) {
 // lane quarters.  CTA r stages tokens [128 r, 128 r + 128) and weight rows [128 r,
 // 128 r + 128) of the tile, and holds its tokens' outputs.  Tiles go round the
 // pairs, tokens fastest, so that the pairs at work share weight tiles in L2.
-constexpr int P8_STAGES = 6;
+constexpr int P8_STAGES = 4;  // (6 measured the same)
 constexpr int P8_HALF = 128 * 128;  // bytes of tokens (or weight rows) per CTA and stage
 constexpr int P8_STAGE = 2 * P8_HALF;
 constexpr int P8_THREADS = 384;
 constexpr int P8_EPI_WARPS = 8;
-constexpr int P8_OUT = 32 * 128;  // bytes that a warp stages of its outputs
-constexpr int P8_SMEM = P8_STAGES * P8_STAGE + P8_EPI_WARPS * P8_OUT + 256 + 1024;
+constexpr int P8_ROW = 256;           // bytes of a row that are written at a time
+constexpr int P8_BOXES = P8_ROW / 128;
+constexpr int P8_OUT = P8_ROW + 16;   // a lane's shared memory: a copy may start inside a unit
+constexpr int P8_SMEM = P8_STAGES * P8_STAGE + P8_EPI_WARPS * 32 * P8_OUT + 256 + 1024;
 
-// Writes 32 rows (one per lane, from row0) of COLS = 128 / sizeof(TO)
-// consecutive outputs from column col: through the warp's shared memory, a
-// row's 16-byte units permuted by the row so that neither side meets a bank
-// twice, and from there in whole row pieces (a lane that stored its own row
-// would touch 32 lines an instruction).
+// A warp's outputs leave through its shared memory, by copies that run while the
+// next tile is computed.  (A lane that stored its row itself would touch 32 lines
+// an instruction; rows written by whole warps cost more instructions than the
+// tile's additions when N is odd.)
+//
+// Where D's rows start on 16-byte boundaries: PIECES boxes of 32 rows x 128
+// bytes, a row's 16-byte units permuted by the row as TMA's 128-byte swizzle has
+// them.  Called by all lanes (lane = row); v holds the lane's outputs.
 template <typename TO>
-__device__ __forceinline__ void p8_store(const Fp8Gemm& g, uint8_t* buf, int row0, int col,
-                                         const float* v, int lane) {
-  constexpr int COLS = 128 / sizeof(TO);
-  if (col >= g.N) return;
-  const int lim = min(COLS, g.N - col);
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    uint4 w;
-    if constexpr (sizeof(TO) == 2) {
-      w.x = pack_bf16x2(v[8 * u + 0], v[8 * u + 1]);
-      w.y = pack_bf16x2(v[8 * u + 2], v[8 * u + 3]);
-      w.z = pack_bf16x2(v[8 * u + 4], v[8 * u + 5]);
-      w.w = pack_bf16x2(v[8 * u + 6], v[8 * u + 7]);
-    } else {
-      w = make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]),
-                     __float_as_uint(v[4 * u + 2]), __float_as_uint(v[4 * u + 3]));
-    }
-    *reinterpret_cast<uint4*>(buf + lane * 128 + ((u ^ (lane & 7)) * 16)) = w;
-  }
+__device__ __forceinline__ void p8_write_boxes(const CUtensorMap* map, const Fp8Gemm& g,
+                                               uint8_t* buf, const float* v, int row0, int col,
+                                               int lane) {
+  constexpr int COLS = 128 / static_cast<int>(sizeof(TO));
+  if (lane == 0) bulk_wait_read();  // the last copies have left the buffer
   __syncwarp();
-  TO* d0 = static_cast<TO*>(g.D) + static_cast<size_t>(row0) * g.N + col;
-  const int rows = min(32, g.M - row0);
-  if (g.vec) {  // rows start on 16-byte boundaries and hold whole units
-    const int u = lane & 7;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = i * 4 + (lane >> 3);
-      const uint4 w = *reinterpret_cast<const uint4*>(buf + r * 128 + ((u ^ (r & 7)) * 16));
-      if (r < rows && u * (16 / static_cast<int>(sizeof(TO))) < lim)
-        *reinterpret_cast<uint4*>(d0 + static_cast<size_t>(r) * g.N +
-                                  u * (16 / sizeof(TO))) = w;
+  for (int q = 0; q < P8_BOXES; ++q) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float* x = v + q * COLS + u * (COLS / 8);
+      uint4 w;
+      if constexpr (sizeof(TO) == 2)
+        w = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                       pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+      else
+        w = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                       __float_as_uint(x[3]));
+      *reinterpret_cast<uint4*>(buf + q * 4096 + lane * 128 + ((u ^ (lane & 7)) * 16)) = w;
     }
+  }
+  fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0) {
+#pragma unroll
+    for (int q = 0; q < P8_BOXES; ++q)
+      if (col + q * COLS < g.N) tma_store_2d(map, buf + q * 4096, col + q * COLS, row0);
+    bulk_commit();
+  }
+}
+
+// Elsewhere: `count` consecutive outputs of one row, v, to d.  The lane puts them
+// into its own piece of shared memory, at the place in a 16-byte unit that they
+// have in D, and hands the whole units to one copy; what fills no unit is stored
+// directly.
+template <typename TO>
+__device__ __forceinline__ void p8_write_row(TO* d, uint8_t* buf, const float* v, int count) {
+  constexpr int W = P8_ROW / 4;
+  uint32_t w[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if constexpr (sizeof(TO) == 2) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    else w[i] = __float_as_uint(v[i]);
+  }
+  const uint32_t ph = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(d)) & 15u;
+  bulk_wait_read();  // the lane's last copy has left the buffer
+  uint32_t* b = reinterpret_cast<uint32_t*>(buf) + (ph >> 2);
+  if constexpr (sizeof(TO) == 2) {
+    // between two words: each takes a half of its neighbour
+    const uint32_t sel = (ph & 2u) ? 0x5432u : 0x7654u;
+    b[0] = __byte_perm(0u, w[0], sel);
+#pragma unroll
+    for (int i = 1; i < W; ++i) b[i] = __byte_perm(w[i - 1], w[i], sel);
+    b[W] = w[W - 1] >> 16;  // (counts where the row starts between two words)
   } else {
-#pragma unroll 4
-    for (int r = 0; r < rows; ++r) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(
-          buf + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4);
-      TO* d = d0 + static_cast<size_t>(r) * g.N;
-      if constexpr (sizeof(TO) == 4) {
-        if (lane < lim) d[lane] = __uint_as_float(w);
-      } else {
-        uint16_t* h = reinterpret_cast<uint16_t*>(d);
-        if ((reinterpret_cast<uintptr_t>(d) & 2) == 0) {
-          if (2 * lane + 1 < lim) *reinterpret_cast<uint32_t*>(h + 2 * lane) = w;
-          else if (2 * lane < lim) h[2 * lane] = static_cast<uint16_t>(w);
-        } else {  // pairs from the second output on; the ends one by one
-          const uint32_t next = __shfl_down_sync(0xffffffffu, w, 1);
-          if (lane < 31 && 2 * lane + 2 < lim)
-            *reinterpret_cast<uint32_t*>(h + 2 * lane + 1) = (w >> 16) | (next << 16);
-          else if (2 * lane + 1 < lim) h[2 * lane + 1] = static_cast<uint16_t>(w >> 16);
-          if (lane == 0) h[0] = static_cast<uint16_t>(w);
-        }
-      }
-    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) b[i] = w[i];
   }
-  __syncwarp();
+  uint8_t* base = reinterpret_cast<uint8_t*>(d) - ph;  // of the unit that d lies in
+  const uint32_t end = ph + static_cast<uint32_t>(count) * sizeof(TO);
+  const uint32_t first = ph ? 16u : 0u, last = end & ~15u;
+  if (last > first) {
+    fence_proxy_async_shared();
+    bulk_store_1d(base + first, buf + first, last - first);
+  }
+  bulk_commit();
+  auto piece = [&](uint32_t at, uint32_t n) {  // n = 2, 4 or 8 bytes, aligned to n
+    if (n == 8) *reinterpret_cast<uint2*>(base + at) = *reinterpret_cast<const uint2*>(buf + at);
+    else if (n == 4)
+      *reinterpret_cast<uint32_t*>(base + at) = *reinterpret_cast<const uint32_t*>(buf + at);
+    else *reinterpret_cast<uint16_t*>(base + at) = *reinterpret_cast<const uint16_t*>(buf + at);
+  };
+  if (ph != 0 && end >= 16u) {  // up to the first boundary: 2, 4, 8 as they fit
+    uint32_t at = ph;
+#pragma unroll
+    for (uint32_t n = sizeof(TO); n <= 8; n *= 2)
+      if (at & n) {
+        piece(at, n);
+        at += n;
+      }
+  }
+  uint32_t at = end >= 16u ? last : ph;  // from the last boundary (or all of it)
+  if (end >= 16u || ph == 0) {
+#pragma unroll
+    for (uint32_t n = 8; n >= sizeof(TO); n /= 2)
+      if (end & n) {
+        piece(at, n);
+        at += n;
+      }
+  } else {  // within one unit, from its middle
+    for (; at < end; at += sizeof(TO)) piece(at, sizeof(TO));
+  }
 }
 
 template <typename TO>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
     k_fp8_pair(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
-               const __grid_constant__ Fp8Gemm g) {
+               const __grid_constant__ CUtensorMap mapD, const __grid_constant__ Fp8Gemm g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* ring = smem;  // stage: tokens, then weight rows
   uint8_t* outs = ring + P8_STAGES * P8_STAGE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(outs + P8_EPI_WARPS * P8_OUT);  // even CTA's are used
+  uint64_t* full = reinterpret_cast<uint64_t*>(outs + P8_EPI_WARPS * 32 * P8_OUT);  // even CTA's are used
   uint64_t* empty = full + P8_STAGES;   // each CTA
   uint64_t* tfull = empty + P8_STAGES;  // [2] each CTA
   uint64_t* tempty = tfull + 2;         // [2] even CTA's are used
@@ -252,7 +293,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
     const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
     const int nb_last = (g.N - 1) / 128;
-    uint8_t* out = outs + (warp - 4) * P8_OUT;
+    // (boxes start on 1024-byte boundaries, a lane's rows on 16-byte ones)
+    uint8_t* out = outs + (g.vec ? (warp - 4) * 32 * P8_ROW : ((warp - 4) * 32 + lane) * P8_OUT);
     uint32_t it = 0;
     bool ok = true;
     // a token's scales times its weight block's, four blocks at a time, loaded
@@ -329,19 +371,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
           ++it;
         }
       }
-      if (ok && out_row < g.M) {
+      const int cols = min(128, g.N - out_col);
+      if (ok && out_row < g.M && cols > 0) {
         if (g.bias != nullptr) {
           const TO* b = static_cast<const TO*>(g.bias) + out_col;
 #pragma unroll
           for (int i = 0; i < 128; ++i)
-            if (out_col + i < g.N) acc[i] += static_cast<float>(b[i]);
+            if (i < cols) acc[i] += static_cast<float>(b[i]);
         }
-        constexpr int COLS = 128 / sizeof(TO);
+        constexpr int COLS = P8_ROW / sizeof(TO);
+        TO* d = static_cast<TO*>(g.D) + static_cast<size_t>(out_row + lane) * g.N + out_col;
 #pragma unroll
-        for (int c = 0; c < 128 / COLS; ++c)
-          p8_store<TO>(g, out, out_row, out_col + c * COLS, acc + c * COLS, lane);
+        for (int c = 0; c < 128 / COLS; ++c) {
+          if (c * COLS >= cols) break;
+          if (g.vec)
+            p8_write_boxes<TO>(&mapD, g, out, acc + c * COLS, out_row, out_col + c * COLS, lane);
+          else if (out_row + lane < g.M)
+            p8_write_row<TO>(d + c * COLS, out, acc + c * COLS, min(COLS, cols - c * COLS));
+        }
       }
+      __syncwarp();
     }
+    bulk_wait();
   }
   tc_fence_before();
   __syncthreads();

@@ -67,6 +67,21 @@ bool fp8_map(CUtensorMap* m, const void* base, int64_t K, int64_t rows, uint32_t
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Output matrix [M][N] of bf16 or fp32, box 128 bytes x 32 rows, 128-byte swizzle.
+template <typename TO>
+bool out_map(CUtensorMap* m, void* base, int64_t M, int64_t N) {
+  const auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(N) * sizeof(TO)};
+  const cuuint32_t box[2] = {128 / sizeof(TO), 32}, estr[2] = {1, 1};
+  return fn(m, sizeof(TO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+            2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kMaxDevices = 64;
 constexpr size_t kMaxSmem = 227 * 1024;
 
@@ -108,11 +123,13 @@ flkl_status launch_pair(const Fp8Call& c) {
   g.vec = (size_t(g.N) * sizeof(TO)) % 16 == 0 && aligned(g.D, 16);
   const int64_t tiles = int64_t(g.m_tiles) * g.n_tiles;
   if (tiles >= (int64_t(1) << 30)) return FLKL_ERR_UNSUPPORTED;
-  CUtensorMap ma, mb;
+  CUtensorMap ma, mb, md;
   if (!fp8_map(&ma, c.A, c.K, g.M, 128) || !fp8_map(&mb, c.B, c.K, g.N, 128))
     return FLKL_ERR_CUDA;
+  md = ma;  // (not used where the rows of D are not on 16-byte boundaries)
+  if (g.vec && !out_map<TO>(&md, g.D, g.M, g.N)) return FLKL_ERR_CUDA;
   const int pairs = static_cast<int>(std::min<int64_t>(device_sms() / 2, tiles));
-  k_fp8_pair<TO><<<2 * pairs, P8_THREADS, P8_SMEM, c.st>>>(ma, mb, g);
+  k_fp8_pair<TO><<<2 * pairs, P8_THREADS, P8_SMEM, c.st>>>(ma, mb, md, g);
   return launched();
 }
 

@@ -238,6 +238,24 @@ def test_block_matmul_empty_out_and_non_finite():
     assert torch.equal(got[[0, 1, 4]], d[[0, 1, 4]])
 
 
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("N", [1, 5, 64, 131, 250, 264])
+def test_block_matmul_output_at_any_place(out, N):
+    """D that starts anywhere in a 16-byte unit, rows of any phase: the outputs
+    are the same and nothing beside them is touched."""
+    from lm_head_projection_b200 import fp8
+
+    for M in (129, 300):
+        qa, sa, qb, sb, want = _product(M, N, 272, out, True)
+        _, _, _, _, plain = _product(M, N, 272, out, False)
+        for off in (0, 1, 3, 7):
+            buf = torch.full((M * N + 24,), 7.0, dtype=DT[out], device="cuda")
+            d = buf[off:off + M * N].view(M, N)
+            fp8.block_matmul(qa, sa, qb, sb, out_dtype=DT[out], out=d)
+            assert torch.equal(d, plain)
+            assert (buf[:off] == 7).all() and (buf[off + M * N:] == 7).all()
+
+
 @pytest.mark.parametrize("M", [3, 130])
 def test_block_matmul_rows_do_not_depend_on_the_batch(M):
     """Twice the same, and (within one kernel's range of M) a row's result does
