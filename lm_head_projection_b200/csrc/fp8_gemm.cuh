@@ -11,10 +11,11 @@
 //   k_fp8_pair    many tokens: 256 tokens x 256 weight rows per CTA pair
 //                 (cta_group::2), a TMEM lane holds one token; bound by the
 //                 tensor cores' rate.
-//   k_fp8_skinny  up to 128 tokens: the weight's rows are the MMA's M side, 128
-//                 per tile, the tokens its N side (16 .. 128 columns), so that
-//                 each weight byte is read once and little of an MMA is
-//                 padding; bound by HBM.
+//   k_fp8_skinny  few tokens: the weight's rows are the MMA's M side, 128 per
+//                 tile, the tokens its N side (16 .. 64 columns), so that each
+//                 weight byte is read once and little of an MMA is padding;
+//                 bound by HBM.  Also more tokens, in tiles of 64, where the
+//                 pairs' tiles would leave most SMs idle.
 //
 // Every wait is bounded; on a timeout the CTA stops computing, lets its copies
 // and MMAs land, frees TMEM and returns, and the status word says so.
@@ -407,7 +408,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
 // 6 warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 2 .. 5 the epilogue,
 // one per TMEM lane quarter (lane = weight row, BN columns = tokens).  The
 // tokens' scales stand in shared memory for the whole call, [kb][BN].  CTAs
-// take tiles of 128 weight rows in turn.  Where there are too few tiles to
+// take tiles of 128 weight rows in turn; more than one token tile makes one CTA
+// (or cluster) per tile.  Where there are too few tiles to
 // keep the SMs reading, a cluster of CTAs shares one tile: CTA r takes its
 // r-th part of K, and the parts' fp32 sums are added in rank order through the
 // cluster's shared memory.
@@ -456,7 +458,9 @@ __global__ void __launch_bounds__(S8_THREADS, 1)
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cs));
   const int kb0 = static_cast<int>(static_cast<long long>(g.KB) * rank / cs);
   const int kb1 = static_cast<int>(static_cast<long long>(g.KB) * (rank + 1) / cs);
-  const int first = blockIdx.x / cs, step = gridDim.x / cs;  // (a cluster has one tile)
+  const int first = blockIdx.x / cs, step = gridDim.x / cs;
+  const int tiles = g.n_tiles * g.m_tiles;
+  const int m0 = first % g.m_tiles * BN;  // (more than one token tile: one tile per CTA)
   constexpr int kCols = s8_tmem_cols<BN>();
 
   if (threadIdx.x == 0) {
@@ -481,7 +485,7 @@ __global__ void __launch_bounds__(S8_THREADS, 1)
   if (warp >= 2) {
     for (int i = threadIdx.x - 64; i < (kb1 - kb0) * BN; i += 128) {
       const int c = i % BN, kb = i / BN;
-      xs[i] = c < g.M ? g.sa[static_cast<size_t>(c) * g.KB + kb0 + kb] : 0.f;
+      xs[i] = m0 + c < g.M ? g.sa[static_cast<size_t>(m0 + c) * g.KB + kb0 + kb] : 0.f;
     }
   }
   tc_fence_before();
@@ -495,7 +499,7 @@ __global__ void __launch_bounds__(S8_THREADS, 1)
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = first; t < g.n_tiles && ok; t += step) {
+      for (int t = first; t < tiles && ok; t += step) {
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) {
             ok = false;
@@ -503,8 +507,8 @@ __global__ void __launch_bounds__(S8_THREADS, 1)
           }
           uint8_t* dst = ring + stage * s8_stage_bytes<BN>();
           mbar_arrive_expect_tx(&full[stage], s8_stage_bytes<BN>());
-          tma_load_2d(&mapW, &full[stage], dst, kb * 128, t * 128);
-          tma_load_2d(&mapX, &full[stage], dst + S8_W, kb * 128, 0);
+          tma_load_2d(&mapW, &full[stage], dst, kb * 128, t / g.m_tiles * 128);
+          tma_load_2d(&mapX, &full[stage], dst + S8_W, kb * 128, m0);
           ++issued;
           if (++stage == S) {
             stage = 0;
@@ -532,7 +536,7 @@ __global__ void __launch_bounds__(S8_THREADS, 1)
       int stage = 0;
       uint32_t phase = 0, it = 0;
       bool ok = true;
-      for (int t = first; t < g.n_tiles && ok; t += step) {
+      for (int t = first; t < tiles && ok; t += step) {
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const uint32_t buf = it % S8_BUFS;
           if (!mbar_wait(&tempty[buf], ((it / S8_BUFS) & 1) ^ 1u, wc) ||
@@ -565,8 +569,8 @@ __global__ void __launch_bounds__(S8_THREADS, 1)
   if (warp >= 2) {
     const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     uint32_t it = 0;
-    for (int t = first; t < g.n_tiles && ok; t += step) {
-      const float* sb = g.sb + static_cast<size_t>(t) * g.KB;
+    for (int t = first; t < tiles && ok; t += step) {
+      const float* sb = g.sb + static_cast<size_t>(t / g.m_tiles) * g.KB;
 #pragma unroll
       for (int i = 0; i < BN / 2; ++i) acc[i] = 0;
       float s_next = __ldg(sb + kb0);
@@ -607,16 +611,16 @@ __global__ void __launch_bounds__(S8_THREADS, 1)
         }
       }
       if (cs == 1 && ok) {
-        const int n = t * 128 + quad * 32 + lane;
+        const int n = t / g.m_tiles * 128 + quad * 32 + lane;
         if (n < g.N) {
           const float b =
               g.bias != nullptr ? static_cast<float>(static_cast<const TO*>(g.bias)[n]) : 0.f;
-          TO* d = static_cast<TO*>(g.D) + n;
+          TO* d = static_cast<TO*>(g.D) + static_cast<size_t>(m0) * g.N + n;
 #pragma unroll
           for (int i = 0; i < BN / 2; ++i) {
             const float2 p = f2_unpack(acc[i]);
-            if (2 * i < g.M) d[static_cast<size_t>(2 * i) * g.N] = fp8_out<TO>(p.x + b);
-            if (2 * i + 1 < g.M) d[static_cast<size_t>(2 * i + 1) * g.N] = fp8_out<TO>(p.y + b);
+            if (m0 + 2 * i < g.M) d[static_cast<size_t>(2 * i) * g.N] = fp8_out<TO>(p.x + b);
+            if (m0 + 2 * i + 1 < g.M) d[static_cast<size_t>(2 * i + 1) * g.N] = fp8_out<TO>(p.y + b);
           }
         }
         __syncwarp();
@@ -643,19 +647,36 @@ __global__ void __launch_bounds__(S8_THREADS, 1)
     cluster_sync();
     // CTA r adds and stores tokens r, r + cs, ...
     if (warp >= 2 && ok) {
-      const int l = quad * 32 + lane, n = first * 128 + l;
+      const int l = quad * 32 + lane, n = first / g.m_tiles * 128 + l;
       if (n < g.N) {
         const float b =
             g.bias != nullptr ? static_cast<float>(static_cast<const TO*>(g.bias)[n]) : 0.f;
-        for (int c = static_cast<int>(rank); c < g.M; c += static_cast<int>(cs)) {
-          const uint32_t at = smem_u32(part + c * 128 + l);
-          float v = 0.f;
-          for (uint32_t r = 0; r < cs; ++r) {
-            float p;
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(mapa_shared(at, r)));
-            v += p;
+        // 4 tokens at a time: their loads from the other CTAs fly together
+        for (int c0 = static_cast<int>(rank); c0 < BN && m0 + c0 < g.M;
+             c0 += 4 * static_cast<int>(cs)) {
+          float p[4][S8_MAX_CLUSTER];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int c = c0 + q * static_cast<int>(cs);
+            const uint32_t at = smem_u32(part + (c < BN ? c : c0) * 128 + l);
+#pragma unroll
+            for (uint32_t r = 0; r < S8_MAX_CLUSTER; ++r) {
+              p[q][r] = 0.f;
+              if (r < cs)
+                asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                             : "=f"(p[q][r])
+                             : "r"(mapa_shared(at, r)));
+            }
           }
-          static_cast<TO*>(g.D)[static_cast<size_t>(c) * g.N + n] = fp8_out<TO>(v + b);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int c = c0 + q * static_cast<int>(cs);
+            float v = p[q][0];
+#pragma unroll
+            for (int r = 1; r < S8_MAX_CLUSTER; ++r) v += p[q][r];
+            if (c < BN && m0 + c < g.M)
+              static_cast<TO*>(g.D)[static_cast<size_t>(m0 + c) * g.N + n] = fp8_out<TO>(v + b);
+          }
         }
       }
     }

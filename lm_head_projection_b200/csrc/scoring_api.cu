@@ -106,6 +106,31 @@ bool raise_smem(K kern, bool (&done)[kMaxDevices]) {
   return done[dev];
 }
 
+// Clusters of `size` CTAs, one CTA to an SM, that are resident at once (a cluster
+// sits inside one GPC, and these differ): 148 SMs hold fewer than 148 / size.
+int resident_clusters(int size) {
+  static int cache[kMaxDevices][S8_MAX_CLUSTER + 1] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 1;
+  if (cache[dev][size] > 0) return cache[dev][size];
+  static bool done[kMaxDevices];
+  int n = 0;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(size * device_sms()));
+  cfg.blockDim = dim3(S8_THREADS);
+  cfg.dynamicSmemBytes = kMaxSmem;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(size);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (!raise_smem(k_fp8_skinny<float, 16>, done) ||
+      cudaOccupancyMaxActiveClusters(&n, k_fp8_skinny<float, 16>, &cfg) != cudaSuccess || n < 1)
+    n = 1;
+  return cache[dev][size] = n;
+}
+
 struct Fp8Call {
   const void *A, *B;
   int64_t K;
@@ -128,7 +153,7 @@ flkl_status launch_pair(const Fp8Call& c) {
     return FLKL_ERR_CUDA;
   md = ma;  // (not used where the rows of D are not on 16-byte boundaries)
   if (g.vec && !out_map<TO>(&md, g.D, g.M, g.N)) return FLKL_ERR_CUDA;
-  const int pairs = static_cast<int>(std::min<int64_t>(device_sms() / 2, tiles));
+  const int pairs = static_cast<int>(std::min<int64_t>(resident_clusters(2), tiles));
   k_fp8_pair<TO><<<2 * pairs, P8_THREADS, P8_SMEM, c.st>>>(ma, mb, md, g);
   return launched();
 }
@@ -138,14 +163,16 @@ flkl_status launch_skinny(const Fp8Call& c, int cluster) {
   static bool done[kMaxDevices];
   if (!raise_smem(k_fp8_skinny<TO, BN>, done)) return FLKL_ERR_CUDA;
   Fp8Gemm g = c.g;
-  g.n_tiles = (g.N + 127) / 128;
+  g.m_tiles = (g.M - 1) / BN + 1;
+  g.n_tiles = (g.N - 1) / 128 + 1;
   const size_t fixed = s8_smem_fixed<BN>((g.KB + cluster - 1) / cluster);
   const size_t stages = std::min<size_t>((kMaxSmem - fixed) / s8_stage_bytes<BN>(), S8_MAX_STAGES);
   g.stages = static_cast<int>(stages);
   CUtensorMap mx, mw;
   if (!fp8_map(&mx, c.A, c.K, g.M, BN) || !fp8_map(&mw, c.B, c.K, g.N, 128)) return FLKL_ERR_CUDA;
+  const int tiles = g.n_tiles * g.m_tiles;
   const int ctas =
-      cluster == 1 ? std::min(device_sms(), g.n_tiles) : g.n_tiles * cluster;
+      cluster == 1 && g.m_tiles == 1 ? std::min(device_sms(), tiles) : tiles * cluster;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(S8_THREADS);
@@ -161,20 +188,27 @@ flkl_status launch_skinny(const Fp8Call& c, int cluster) {
                                                                                  : FLKL_ERR_CUDA;
 }
 
+// Which kernel.  A pair's 256 x 256 tile holds 8 of the small kernel's 128 x 64
+// tiles on two SMs and takes about as long per block of K, so that it wins where
+// a quarter of the pairs have a tile: 128 x 14336 x 4096 24 against 32 us, 129 x
+// 1000 x 8192 36 against 18 us.  Up to 64 rows there is one token tile and the
+// weight is streamed at HBM's rate (64 x 128256 x 4096: 108 us, pairs 139 us).
 template <typename TO>
 flkl_status fp8_matmul(const Fp8Call& c) {
   const int M = c.g.M, KB = c.g.KB, sms = device_sms();
-  if (M <= 128) {
-    // CTAs that share a tile of 128 weight rows: as many as leave none idle
-    const int n_tiles = (c.g.N + 127) / 128;
-    const int cluster = std::max(1, std::min({S8_MAX_CLUSTER, sms / n_tiles, KB}));
-    const int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-    // (the tokens' scales have to leave room for three stages and the parts)
-    if (s8_smem_fixed<128>((KB + cluster - 1) / cluster) + 4 * s8_stage_bytes<128>() <= kMaxSmem) {
-      if (bn == 16) return launch_skinny<TO, 16>(c, cluster);
-      if (bn == 32) return launch_skinny<TO, 32>(c, cluster);
-      if (bn == 64) return launch_skinny<TO, 64>(c, cluster);
-      return launch_skinny<TO, 128>(c, cluster);
+  const int64_t pair_tiles = int64_t((M - 1) / 256 + 1) * ((c.g.N - 1) / 256 + 1);
+  if (M <= 64 || pair_tiles <= sms / 8) {
+    // CTAs that share a tile, each with a part of K: as many as run at once
+    const int64_t tiles = int64_t((c.g.N - 1) / 128 + 1) * ((M - 1) / 64 + 1);
+    int cluster = static_cast<int>(std::min<int64_t>({S8_MAX_CLUSTER, sms / tiles, KB}));
+    while (cluster > 1 && resident_clusters(cluster) < tiles) --cluster;
+    cluster = std::max(cluster, 1);
+    // (the tokens' scales have to leave room for a ring, which later holds the
+    // cluster's parts)
+    if (s8_smem_fixed<64>((KB + cluster - 1) / cluster) + 4 * s8_stage_bytes<64>() <= kMaxSmem) {
+      if (M <= 16) return launch_skinny<TO, 16>(c, cluster);
+      if (M <= 32) return launch_skinny<TO, 32>(c, cluster);
+      return launch_skinny<TO, 64>(c, cluster);
     }
   }
   return launch_pair<TO>(c);
