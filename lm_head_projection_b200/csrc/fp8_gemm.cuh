@@ -405,20 +405,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
 }
 
 // ----------------------------------------------------------------- skinny
-// 6 warps: 0 TMA producer, 1 TMEM owner and MMA issuer, 2 .. 5 the epilogue,
-// one per TMEM lane quarter (lane = weight row, BN columns = tokens).  The
+// Warps: 0 TMA producer, 1 TMEM owner and MMA issuer, from 2 on the epilogue, four
+// (one per TMEM lane quarter; lane = weight row, column = token) for each group of
+// s8_cols columns: with 64 tokens, one group's work on a block would take longer
+// than the block's load (113 against 95 us with 128256 x 4096).  The
 // tokens' scales stand in shared memory for the whole call, [kb][BN].  CTAs
 // take tiles of 128 weight rows in turn; more than one token tile makes one CTA
 // (or cluster) per tile.  Where there are too few tiles to
 // keep the SMs reading, a cluster of CTAs shares one tile: CTA r takes its
 // r-th part of K, and the parts' fp32 sums are added in rank order through the
 // cluster's shared memory.
-constexpr int S8_THREADS = 192;
 constexpr int S8_W = 128 * 128;  // weight bytes per stage
 constexpr int S8_MAX_STAGES = 16;
 constexpr int S8_BUFS = 4;       // TMEM buffers of BN columns
 constexpr int S8_MAX_CLUSTER = 8;
 
+template <int BN>
+__host__ __device__ constexpr int s8_cols() { return BN > 32 ? 32 : BN; }
+template <int BN>
+__host__ __device__ constexpr int s8_threads() { return 64 + 128 * (BN / s8_cols<BN>()); }
 template <int BN>
 __host__ __device__ constexpr int s8_stage_bytes() { return S8_W + BN * 128; }
 template <int BN>
@@ -435,7 +440,7 @@ __host__ __device__ constexpr size_t s8_smem_fixed(size_t kbs) {
 }
 
 template <typename TO, int BN>
-__global__ void __launch_bounds__(S8_THREADS, 1)
+__global__ void __launch_bounds__(s8_threads<BN>(), 1)
     k_fp8_skinny(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapW,
                  const __grid_constant__ Fp8Gemm g) {
   extern __shared__ uint8_t smem_raw[];
@@ -470,7 +475,7 @@ __global__ void __launch_bounds__(S8_THREADS, 1)
     }
     for (int a = 0; a < S8_BUFS; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 4);
+      mbar_init(&tempty[a], 4 * (BN / s8_cols<BN>()));
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -483,7 +488,7 @@ __global__ void __launch_bounds__(S8_THREADS, 1)
     tmem_relinquish();
   }
   if (warp >= 2) {
-    for (int i = threadIdx.x - 64; i < (kb1 - kb0) * BN; i += 128) {
+    for (int i = threadIdx.x - 64; i < (kb1 - kb0) * BN; i += blockDim.x - 64) {
       const int c = i % BN, kb = i / BN;
       xs[i] = m0 + c < g.M ? g.sa[static_cast<size_t>(m0 + c) * g.KB + kb0 + kb] : 0.f;
     }
@@ -564,33 +569,34 @@ __global__ void __launch_bounds__(S8_THREADS, 1)
     __syncwarp();
   }
   bool ok = true;
-  uint64_t acc[BN / 2];
-  const int quad = warp & 3;
+  constexpr int CN = s8_cols<BN>();
+  uint64_t acc[CN / 2];
+  const int quad = warp & 3, col0 = (warp - 2) / 4 * CN;
   if (warp >= 2) {
-    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16) + col0;
     uint32_t it = 0;
     for (int t = first; t < tiles && ok; t += step) {
       const float* sb = g.sb + static_cast<size_t>(t / g.m_tiles) * g.KB;
 #pragma unroll
-      for (int i = 0; i < BN / 2; ++i) acc[i] = 0;
+      for (int i = 0; i < CN / 2; ++i) acc[i] = 0;
       float s_next = __ldg(sb + kb0);
       for (int kb = kb0; kb < kb1; ++kb, ++it) {
         const uint32_t buf = it % S8_BUFS;
         const uint64_t s = f2_pack(s_next, s_next);
         if (kb + 1 < kb1) s_next = __ldg(sb + kb + 1);
-        if (!mbar_wait(&tfull[buf], (it / S8_BUFS) & 1, wc)) {
+        ok = mbar_wait(&tfull[buf], (it / S8_BUFS) & 1, wc);
+        if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
-        __syncwarp();
         tc_fence_after();
-        const ulonglong2* x2 = reinterpret_cast<const ulonglong2*>(xs + (kb - kb0) * BN);
+        const ulonglong2* x2 = reinterpret_cast<const ulonglong2*>(xs + (kb - kb0) * BN + col0);
         uint32_t r[2][16];
         tmem_ld16_async(tl + buf * BN, r[0]);
 #pragma unroll
-        for (int c = 0; c < BN / 16; ++c) {
+        for (int c = 0; c < CN / 16; ++c) {
           tmem_wait16(r[c & 1]);
-          if (c + 1 < BN / 16) {
+          if (c + 1 < CN / 16) {
             tmem_ld16_async(tl + buf * BN + (c + 1) * 16, r[(c + 1) & 1]);
           } else {
             tc_fence_before();
@@ -615,12 +621,13 @@ __global__ void __launch_bounds__(S8_THREADS, 1)
         if (n < g.N) {
           const float b =
               g.bias != nullptr ? static_cast<float>(static_cast<const TO*>(g.bias)[n]) : 0.f;
-          TO* d = static_cast<TO*>(g.D) + static_cast<size_t>(m0) * g.N + n;
+          const int m = m0 + col0;
+          TO* d = static_cast<TO*>(g.D) + static_cast<size_t>(m) * g.N + n;
 #pragma unroll
-          for (int i = 0; i < BN / 2; ++i) {
+          for (int i = 0; i < CN / 2; ++i) {
             const float2 p = f2_unpack(acc[i]);
-            if (m0 + 2 * i < g.M) d[static_cast<size_t>(2 * i) * g.N] = fp8_out<TO>(p.x + b);
-            if (m0 + 2 * i + 1 < g.M) d[static_cast<size_t>(2 * i + 1) * g.N] = fp8_out<TO>(p.y + b);
+            if (m + 2 * i < g.M) d[static_cast<size_t>(2 * i) * g.N] = fp8_out<TO>(p.x + b);
+            if (m + 2 * i + 1 < g.M) d[static_cast<size_t>(2 * i + 1) * g.N] = fp8_out<TO>(p.y + b);
           }
         }
         __syncwarp();
@@ -638,27 +645,27 @@ __global__ void __launch_bounds__(S8_THREADS, 1)
     float* part = reinterpret_cast<float*>(ring);
     if (warp >= 2) {
 #pragma unroll
-      for (int i = 0; i < BN / 2; ++i) {
+      for (int i = 0; i < CN / 2; ++i) {
         const float2 p = f2_unpack(acc[i]);
-        part[(2 * i) * 128 + quad * 32 + lane] = p.x;
-        part[(2 * i + 1) * 128 + quad * 32 + lane] = p.y;
+        part[(col0 + 2 * i) * 128 + quad * 32 + lane] = p.x;
+        part[(col0 + 2 * i + 1) * 128 + quad * 32 + lane] = p.y;
       }
     }
     cluster_sync();
-    // CTA r adds and stores tokens r, r + cs, ...
+    // CTA r adds and stores tokens r, r + cs, ... of each group
     if (warp >= 2 && ok) {
       const int l = quad * 32 + lane, n = first / g.m_tiles * 128 + l;
       if (n < g.N) {
         const float b =
             g.bias != nullptr ? static_cast<float>(static_cast<const TO*>(g.bias)[n]) : 0.f;
         // 4 tokens at a time: their loads from the other CTAs fly together
-        for (int c0 = static_cast<int>(rank); c0 < BN && m0 + c0 < g.M;
+        for (int c0 = static_cast<int>(rank) + col0; c0 < col0 + CN && m0 + c0 < g.M;
              c0 += 4 * static_cast<int>(cs)) {
           float p[4][S8_MAX_CLUSTER];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int c = c0 + q * static_cast<int>(cs);
-            const uint32_t at = smem_u32(part + (c < BN ? c : c0) * 128 + l);
+            const uint32_t at = smem_u32(part + (c < col0 + CN ? c : c0) * 128 + l);
 #pragma unroll
             for (uint32_t r = 0; r < S8_MAX_CLUSTER; ++r) {
               p[q][r] = 0.f;
@@ -674,7 +681,7 @@ __global__ void __launch_bounds__(S8_THREADS, 1)
             float v = p[q][0];
 #pragma unroll
             for (int r = 1; r < S8_MAX_CLUSTER; ++r) v += p[q][r];
-            if (c < BN && m0 + c < g.M)
+            if (c < col0 + CN && m0 + c < g.M)
               static_cast<TO*>(g.D)[static_cast<size_t>(m0 + c) * g.N + n] = fp8_out<TO>(v + b);
           }
         }

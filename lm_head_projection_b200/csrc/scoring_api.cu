@@ -117,7 +117,7 @@ int resident_clusters(int size) {
   int n = 0;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(size * device_sms()));
-  cfg.blockDim = dim3(S8_THREADS);
+  cfg.blockDim = dim3(s8_threads<16>());
   cfg.dynamicSmemBytes = kMaxSmem;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -175,7 +175,7 @@ flkl_status launch_skinny(const Fp8Call& c, int cluster) {
       cluster == 1 && g.m_tiles == 1 ? std::min(device_sms(), tiles) : tiles * cluster;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(S8_THREADS);
+  cfg.blockDim = dim3(s8_threads<BN>());
   cfg.dynamicSmemBytes = fixed + stages * s8_stage_bytes<BN>();
   cfg.stream = c.st;
   cudaLaunchAttribute at{};
@@ -190,9 +190,10 @@ flkl_status launch_skinny(const Fp8Call& c, int cluster) {
 
 // Which kernel.  A pair's 256 x 256 tile holds 8 of the small kernel's 128 x 64
 // tiles on two SMs and takes about as long per block of K, so that it wins where
-// a quarter of the pairs have a tile: 128 x 14336 x 4096 24 against 32 us, 129 x
-// 1000 x 8192 36 against 18 us.  Up to 64 rows there is one token tile and the
-// weight is streamed at HBM's rate (64 x 128256 x 4096: 108 us, pairs 139 us).
+// a quarter of the pairs have a tile: 128 x 14336 x 4096 takes them 24 us (one
+// tile of 128 tokens in the small kernel: 30), 129 x 1000 x 8192 36 us (18).  Up
+// to 64 rows there is one token tile and the weight is streamed at HBM's rate
+// (64 x 128256 x 4096: 104 us, pairs 133).
 template <typename TO>
 flkl_status fp8_matmul(const Fp8Call& c) {
   const int M = c.g.M, KB = c.g.KB, sms = device_sms();
