@@ -457,7 +457,7 @@ FLKL_API flkl_status flkl_fp8_quantize(const void* src, int64_t rows, int64_t co
  *  B        device [N, K] e4m3, b_scale fp32 [ceil(N / 128), ceil(K / 128)].
  *  bias     device [N], out_dtype, or NULL.
  *  D        device [M, N], out_dtype (overwritten), sums in fp32.
- *  M, N >= 0, K >= 1 a multiple of 16, each below 2^31; A and B 16-byte
+ *  M, N >= 0, K >= 1 a multiple of 16, none above 2^30; A and B 16-byte
  *  aligned, the others to their type; all dense.  Asynchronous on `stream`;
  *  no workspace.  Every wait in the kernels is bounded: after a timeout D is
  *  undefined and flkl_fp8_device_status says so. */
@@ -486,6 +486,7 @@ FLKL_API flkl_status flkl_fp8_device_status(void* stream);
  *              target is ignore_index is dropped: logp, entropy, lse and
  *              top_logp 0, top_ids -1, gradient 0, its logits not read.  A
  *              target outside [0, V) otherwise: logp 0, the rest as usual.
+ *  temperature above 2^-120 and finite.
  *  top_k       0 .. 32, at most V.
  *  entropy, lse   device fp32 [rows]; logp likewise (with target).
  *  stats       device fp32 [rows, 2], 8-byte aligned: the row's largest logit
@@ -499,7 +500,8 @@ FLKL_API flkl_status flkl_fp8_device_status(void* stream);
  * flkl_token_logprobs_backward: the gradient of the logits for upstream
  * gradients dlogp, dentropy [rows] and dtop_logp [rows, top_k] (device fp32,
  * NULL: none), from the forward's stats, entropy and top_ids; the other
- * arguments are the forward's.  dlogits: `dtype`, rows d_row_stride apart. */
+ * arguments are the forward's.  dlogits: `dtype`, rows d_row_stride apart; must
+ * not overlap logits. */
 FLKL_API flkl_status flkl_token_logprobs_forward(const void* logits, int64_t row_stride,
                                                  const int64_t* target, int64_t ignore_index,
                                                  int64_t rows, int64_t V, int dtype,

@@ -466,25 +466,24 @@ def _check_dev(name, t, dtype, shape, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
-def _launch(what: str, call, args, dev, stream: Optional[torch.cuda.Stream]) -> None:
-    """``call(*args, stream)`` on ``stream`` (default: the current one of
-    ``dev``) with ``dev`` as the current device, since the library launches
-    there; raises FlklError on a non-OK status."""
+def _launch(what: str, call, args, dev) -> None:
+    """``call(*args, stream)`` on the current stream of ``dev``, with ``dev`` as
+    the current device, since the library launches there; raises FlklError on a
+    non-OK status.  (Callers that are given a stream make it the current one
+    first, so that what they allocate belongs to it.)"""
     if dev.type != "cuda":
         raise ValueError(f"{what} needs CUDA tensors, got {dev}")
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _launch(what, call, args, dev, stream)
+            return _launch(what, call, args, dev)
     # (the raw handle: a Stream object costs as much as a small launch)
-    st = stream.cuda_stream if stream is not None \
-        else torch._C._cuda_getCurrentRawStream(dev.index)
-    status = call(*args, st)
+    status = call(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     if status != FLKL_OK:
         raise FlklError(status, what)
 

@@ -22,6 +22,8 @@ constexpr int64_t kMaxDim = int64_t(1) << 31;
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool dtype_ok(int d) { return d == FLKL_DTYPE_F32 || d == FLKL_DTYPE_BF16; }
+// (1 / temperature has to be a number too)
+bool temperature_ok(float t) { return t > 0x1p-120f && t < INFINITY; }
 size_t elem_size(int d) { return d == FLKL_DTYPE_F32 ? 4 : 2; }
 flkl_status launched() {
   return cudaGetLastError() == cudaSuccess ? FLKL_OK : FLKL_ERR_CUDA;
@@ -263,7 +265,8 @@ flkl_status flkl_fp8_block_matmul(const void* A, const float* a_scale, const voi
                                   const float* b_scale, const void* bias, int64_t M, int64_t N,
                                   int64_t K, int out_dtype, void* D, void* stream) {
   if (!dtype_ok(out_dtype) || M < 0 || N < 0 || K < 1) return FLKL_ERR_INVALID_ARG;
-  if (K % 16 != 0 || M >= kMaxDim || N >= kMaxDim || K >= kMaxDim) return FLKL_ERR_UNSUPPORTED;
+  if (K % 16 != 0 || M > kMaxDim / 2 || N > kMaxDim / 2 || K > kMaxDim / 2)
+    return FLKL_ERR_UNSUPPORTED;
   if (M == 0 || N == 0) return FLKL_OK;
   if (A == nullptr || B == nullptr || a_scale == nullptr || b_scale == nullptr || D == nullptr)
     return FLKL_ERR_INVALID_ARG;
@@ -309,7 +312,7 @@ flkl_status flkl_token_logprobs_forward(const void* logits, int64_t row_stride,
                                         void* stream) {
   if (!dtype_ok(dtype) || rows < 0 || V < 1 || top_k < 0 || row_stride < V)
     return FLKL_ERR_INVALID_ARG;
-  if (!(temperature > 0.f) || !(temperature < INFINITY)) return FLKL_ERR_INVALID_ARG;
+  if (!temperature_ok(temperature)) return FLKL_ERR_INVALID_ARG;
   if (top_k > LP_MAX_K || top_k > V || rows >= kMaxDim || V >= kMaxDim ||
       row_stride >= (int64_t(1) << 40))
     return FLKL_ERR_UNSUPPORTED;
@@ -353,7 +356,7 @@ flkl_status flkl_token_logprobs_backward(const void* logits, int64_t row_stride,
                                          void* dlogits, int64_t d_row_stride, void* stream) {
   if (!dtype_ok(dtype) || rows < 0 || V < 1 || top_k < 0 || row_stride < V || d_row_stride < V)
     return FLKL_ERR_INVALID_ARG;
-  if (!(temperature > 0.f) || !(temperature < INFINITY)) return FLKL_ERR_INVALID_ARG;
+  if (!temperature_ok(temperature)) return FLKL_ERR_INVALID_ARG;
   if (top_k > LP_MAX_K || top_k > V || rows >= kMaxDim || V >= kMaxDim ||
       row_stride >= (int64_t(1) << 40) || d_row_stride >= (int64_t(1) << 40))
     return FLKL_ERR_UNSUPPORTED;

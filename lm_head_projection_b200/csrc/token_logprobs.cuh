@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(LPB_NT) k_token_logprobs_bwd(const LpBwdArgs a
                        __float_as_uint(f[3]));
       }
     }
-    dv[i] = o;
+    __stcs(dv + i, o);  // (not read again here: 112 -> 108 us for 1024 x 151936 bf16)
   }
   if (none) return;
   __syncthreads();

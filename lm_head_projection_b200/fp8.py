@@ -22,6 +22,9 @@ _F8 = torch.float8_e4m3fn
 
 
 def _quantize(x: torch.Tensor, block_rows: int, stream) -> Tuple[torch.Tensor, torch.Tensor]:
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _quantize(x, block_rows, None)
     if x.dtype not in DTYPES:
         raise ValueError(f"dtype {x.dtype} not supported (float32 or bfloat16)")
     if x.dim() < 2:
@@ -35,7 +38,7 @@ def _quantize(x: torch.Tensor, block_rows: int, stream) -> Tuple[torch.Tensor, t
     scale = x.new_empty(shape, dtype=torch.float32)
     _launch("flkl_fp8_quantize", flkl_fp8_quantize,
             (x.data_ptr(), rows, K, DTYPES[x.dtype], block_rows, q.data_ptr(), scale.data_ptr()),
-            x.device, stream)
+            x.device)
     return q, scale
 
 
@@ -61,6 +64,9 @@ def block_matmul(A: torch.Tensor, a_scale: torch.Tensor, B: torch.Tensor, b_scal
     ``[M, ceil(K / 128)]``) and ``B [N, K]`` (scales ``[ceil(N / 128),
     ceil(K / 128)]``), in ``out_dtype`` (bfloat16 or float32; ``bias [N]`` has
     it too); fp32 sums, one rounding.  K must be a multiple of 16."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return block_matmul(A, a_scale, B, b_scale, bias, out_dtype, out)
     if out_dtype not in DTYPES:
         raise ValueError(f"out_dtype {out_dtype} not supported (float32 or bfloat16)")
     if A.dim() != 2 or B.dim() != 2:
@@ -81,7 +87,7 @@ def block_matmul(A: torch.Tensor, a_scale: torch.Tensor, B: torch.Tensor, b_scal
         _check_dev("out", out, out_dtype, (M, N), dev)
     _launch("flkl_fp8_block_matmul", flkl_fp8_block_matmul,
             (A.data_ptr(), a_scale.data_ptr(), B.data_ptr(), b_scale.data_ptr(), _ptr(bias), M,
-             N, K, DTYPES[out_dtype], out.data_ptr()), dev, stream)
+             N, K, DTYPES[out_dtype], out.data_ptr()), dev)
     return out
 
 

@@ -53,19 +53,24 @@ def token_logprobs_forward(logits: torch.Tensor, target: Optional[torch.Tensor] 
     target outside [0, V) has logp 0.  Masked logits (-infinity) have
     probability 0; a row of nothing else gives logp, lse and top_logp
     -infinity and entropy 0."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return token_logprobs_forward(logits, target, ignore_index, temperature, top_k)
     rows, V, ld = _check_logits(logits, target)
     if not 0 <= top_k <= min(MAX_TOP_K, V):
         raise ValueError(f"top_k must lie in [0, {min(MAX_TOP_K, V)}], got {top_k}")
     dev, f32 = logits.device, torch.float32
-    new = logits.new_empty  # (cheaper than torch.empty)
-    entropy, lse, stats = new(rows, dtype=f32), new(rows, dtype=f32), new((rows, 2), dtype=f32)
-    logp = new(rows, dtype=f32) if target is not None else None
-    top_logp = new((rows, top_k), dtype=f32) if top_k else None
-    top_ids = new((rows, top_k), dtype=torch.int64) if top_k else None
+    # (in the cheapest of torch's ways to allocate: six outputs cost more host
+    # time than the launch)
+    entropy = logits.new_empty(rows, dtype=f32)
+    lse, stats = torch.empty_like(entropy), entropy.new_empty((rows, 2))
+    logp = torch.empty_like(entropy) if target is not None else None
+    top_logp = entropy.new_empty((rows, top_k)) if top_k else None
+    top_ids = logits.new_empty((rows, top_k), dtype=torch.int64) if top_k else None
     _launch("flkl_token_logprobs_forward", flkl_token_logprobs_forward,
             (logits.data_ptr(), ld, _ptr(target), ignore_index, rows, V, DTYPES[logits.dtype],
              temperature, top_k, _ptr(logp), entropy.data_ptr(), lse.data_ptr(),
-             stats.data_ptr(), _ptr(top_logp), _ptr(top_ids)), dev, stream)
+             stats.data_ptr(), _ptr(top_logp), _ptr(top_ids)), dev)
     return {"logp": logp, "entropy": entropy, "lse": lse, "top_logp": top_logp,
             "top_ids": top_ids, "stats": stats}
 
@@ -80,6 +85,10 @@ def token_logprobs_backward(logits: torch.Tensor, target: Optional[torch.Tensor]
     fp32 gradients of logp, entropy ``[rows]`` and top_logp ``[rows, top_k]``
     (None: none), from the dict that :func:`token_logprobs_forward` returned
     for the same logits, target, ignore_index and temperature."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return token_logprobs_backward(logits, target, forward, dlogp, dentropy, dtop_logp,
+                                           ignore_index, temperature)
     rows, V, ld = _check_logits(logits, target)
     dev, f32 = logits.device, torch.float32
     stats, entropy, top_ids = forward["stats"], forward["entropy"], forward["top_ids"]
@@ -102,7 +111,7 @@ def token_logprobs_backward(logits: torch.Tensor, target: Optional[torch.Tensor]
     _launch("flkl_token_logprobs_backward", flkl_token_logprobs_backward,
             (logits.data_ptr(), ld, _ptr(target), ignore_index, rows, V, DTYPES[logits.dtype],
              temperature, k, stats.data_ptr(), entropy.data_ptr(), _ptr(top_ids), _ptr(dlogp),
-             _ptr(dentropy), _ptr(dtop_logp), dlogits.data_ptr(), ld), dev, stream)
+             _ptr(dentropy), _ptr(dtop_logp), dlogits.data_ptr(), ld), dev)
     return dlogits
 
 

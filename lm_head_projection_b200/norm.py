@@ -97,6 +97,9 @@ def add_rms_norm(X: torch.Tensor, W: torch.Tensor, residual: Optional[torch.Tens
     has X's type and scale is None.  Without a residual H is X itself;
     ``inplace`` writes h over the residual.  No gradient is recorded: see
     :class:`AddRMSNorm`."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return add_rms_norm(X, W, residual, eps, quantize, inplace)
     if X.dtype not in DTYPES:
         raise ValueError(f"dtype {X.dtype} not supported (float32 or bfloat16)")
     if X.dim() < 1:
@@ -116,7 +119,7 @@ def add_rms_norm(X: torch.Tensor, W: torch.Tensor, residual: Optional[torch.Tens
     scale = X.new_empty((*X.shape[:-1], -(-H // 128)), dtype=torch.float32) if quantize else None
     _launch("flkl_add_rms_norm_forward", flkl_add_rms_norm_forward,
             (X.data_ptr(), _ptr(residual), W.data_ptr(), rows, H, DTYPES[dt], eps,
-             int(bool(quantize)), Y.data_ptr(), _ptr(scale), _ptr(Hs)), dev, stream)
+             int(bool(quantize)), Y.data_ptr(), _ptr(scale), _ptr(Hs)), dev)
     return {"Y": Y, "scale": scale, "H": X if Hs is None else Hs}
 
 
@@ -127,17 +130,23 @@ def add_rms_norm_backward(dY: torch.Tensor, H: torch.Tensor, W: torch.Tensor,
     """Gradients of :func:`add_rms_norm` from its ``H``: dX, the gradient of X
     and of the residual alike, with ``dH`` (what arrives at h from its other
     use) added; and dW unless the weight is frozen.  Returns ``{"dX", "dW"}``."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return add_rms_norm_backward(dY, H, W, dH, eps, compute_dW, accum_fp32)
     rows, hidden, dev, dt, pdt = _prepare(dY, H, W, accum_fp32)
     if dH is not None:
         _check_dev("dH", dH, dt, H.shape, dev)
     dX = torch.empty_like(H)
     dW = H.new_empty(hidden, dtype=pdt) if compute_dW else None
-    with torch.cuda.device(dev):  # the size goes by the current device
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):  # the size goes by the current device
+            need = flkl_norm_workspace_size(rows, hidden, compute_dW, False)
+    else:
         need = flkl_norm_workspace_size(rows, hidden, compute_dW, False)
     ws = H.new_empty(need, dtype=torch.uint8) if need else None
     _launch("flkl_add_rms_norm_backward", flkl_add_rms_norm_backward,
             (_ptr(dY), _ptr(dH), _ptr(H), _ptr(W), rows, hidden, DTYPES[dt], eps, compute_dW,
-             accum_fp32, _ptr(dX), _ptr(dW), _ptr(ws), need), dev, stream)
+             accum_fp32, _ptr(dX), _ptr(dW), _ptr(ws), need), dev)
     return {"dX": dX, "dW": dW}
 
 

@@ -621,6 +621,39 @@ def test_side_stream_and_captured_graph(rows):
         assert torch.equal(graphs[0][4][k], want2[k]), k
 
 
+def test_calls_with_a_stream_of_their_own():
+    """Every call on the stream it is given, its allocations too, while the
+    current stream is busy with other work."""
+    from lm_head_projection_b200 import fp8, logprobs, norm
+
+    x, r, w = [t.cuda() for t in _norm_inputs(40, 512, "bf16")]
+    z, t = _logits(40, 3000, "bf16", 8)
+    qb, sb = fp8.quantize_blocks(torch.randn(700, 512, device="cuda"))
+
+    def chain(**kw):
+        f = norm.add_rms_norm(x, w, r, quantize=True, **kw)
+        b = norm.add_rms_norm_backward(x, f["H"], w, dH=r, **kw)
+        q, s = fp8.quantize_rows(x, **kw)
+        d = fp8.block_matmul(q, s, qb, sb, **kw)
+        l = logprobs.token_logprobs_forward(z, t, top_k=4, **kw)
+        g = logprobs.token_logprobs_backward(z, t, l, dentropy=l["entropy"], **kw)
+        return [f["Y"].float(), f["scale"], f["H"], b["dX"], b["dW"], q.float(), d, l["logp"], g]
+
+    want = chain()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for _ in range(20):
+            junk = torch.randn(64, 4096, device="cuda") * 2  # what the current stream reuses
+        got.append(chain(stream=side))
+        side.synchronize()
+    torch.cuda.synchronize()
+    for g in got:
+        for a, b in zip(g, want):
+            assert torch.equal(a, b)
+
+
 def test_two_streams_at_once():
     n, head, x, r, t, scorer = _chain()
     sc = scorer()
@@ -638,6 +671,82 @@ def test_two_streams_at_once():
         for o_ in got[i]:
             for k in want[i]:
                 assert torch.equal(o_[k], want[i][k]), k
+
+
+_FIRST_CALLS_IN_A_GRAPH = """
+import sys; sys.path.insert(0, sys.argv[1])
+import torch
+from lm_head_projection_b200 import fp8, logprobs, norm
+g = torch.Generator(device="cuda").manual_seed(0)
+r = lambda *s: torch.randn(*s, device="cuda", generator=g)
+x, h, w, wt, z = r(200, 512).bfloat16(), r(200, 512).bfloat16(), r(512).bfloat16(), r(1000, 512), r(6, 3000)
+t = torch.randint(0, 3000, (6,), device="cuda", generator=g)
+def step():
+    f = norm.add_rms_norm(x, w, h, quantize=True)
+    b = norm.add_rms_norm_backward(x, f["H"], w, dH=h)
+    qb, sb = fp8.quantize_blocks(wt)
+    d = fp8.block_matmul(f["Y"], f["scale"], qb, sb)
+    e = fp8.block_matmul(f["Y"][:9], f["scale"][:9], qb, sb)
+    l = logprobs.token_logprobs_forward(z, t, top_k=3)
+    return [b["dX"], b["dW"], d, e, l["logp"], l["top_ids"],
+            logprobs.token_logprobs_backward(z, t, l, dlogp=l["logp"])]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, step()))
+from lm_head_projection_b200 import flkl_fp8_device_status, flkl_norm_device_status
+assert flkl_fp8_device_status() == 0 and flkl_norm_device_status() == 0
+"""
+
+
+def test_first_calls_of_a_process_inside_a_graph():
+    """Nothing of a first call (attributes, driver entry points, occupancy) is
+    forbidden while a stream is captured."""
+    import subprocess
+    import sys
+    from pathlib import Path
+
+    root = Path(__file__).resolve().parent.parent
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALLS_IN_A_GRAPH, str(root)],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_autograd_step_captured():
+    """The modules' forward and backward in a graph, warmed up on a side stream."""
+    from lm_head_projection_b200.logprobs import TokenLogProbs
+    from lm_head_projection_b200.norm import AddRMSNorm
+
+    m, lp = AddRMSNorm(256, device="cuda"), TokenLogProbs(top_k=3)
+    x, r, w = [t.cuda() for t in _norm_inputs(30, 256, "bf16")]
+    x.requires_grad_()
+    t = torch.randint(0, 256, (30,)).cuda()
+
+    def step():
+        m.weight.grad = x.grad = None
+        y, h = m(x, r)
+        o_ = lp(y, t)
+        (o_.logp.sum() + o_.entropy.sum() + o_.top_logp.sum() + h.float().sum()).backward()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    want = [x.grad.clone(), m.weight.grad.clone()]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    got = [x.grad, m.weight.grad]
+    for v in got:
+        v.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
 
 
 def test_training_step_captured_while_an_eager_one_lives():

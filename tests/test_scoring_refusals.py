@@ -57,7 +57,7 @@ def test_quantize_refusals(kw, want):
 @no_gpu
 @pytest.mark.parametrize("kw,want", [
     (dict(out=2), INVALID), (dict(M=-1), INVALID), (dict(N=-1), INVALID), (dict(K=0), INVALID),
-    (dict(K=24), UNSUPPORTED), (dict(M=1 << 31), UNSUPPORTED), (dict(A=0), INVALID),
+    (dict(K=24), UNSUPPORTED), (dict(M=(1 << 30) + 1), UNSUPPORTED), (dict(A=0), INVALID),
     (dict(B=0), INVALID), (dict(sa=0), INVALID), (dict(sb=0), INVALID), (dict(D=0), INVALID),
     (dict(A=P + 8), UNSUPPORTED), (dict(B=P + 8), UNSUPPORTED), (dict(D=P + 1), UNSUPPORTED),
     (dict(sa=P + 2), UNSUPPORTED), (dict(bias=P + 1), UNSUPPORTED), (dict(M=0, A=0), OK),
@@ -77,7 +77,8 @@ _LP = dict(z=P, ld=64, t=P, rows=4, V=64, dtype=1, T=1.0, k=0, logp=P, ent=P, ls
 @pytest.mark.parametrize("kw,want", [
     (dict(dtype=2), INVALID), (dict(rows=-1), INVALID), (dict(V=0), INVALID),
     (dict(ld=63), INVALID), (dict(T=0.0), INVALID), (dict(T=NAN), INVALID),
-    (dict(T=float("inf")), INVALID), (dict(k=-1), INVALID), (dict(k=33), UNSUPPORTED),
+    (dict(T=float("inf")), INVALID), (dict(T=1e-40), INVALID), (dict(k=-1), INVALID),
+    (dict(k=33), UNSUPPORTED),
     (dict(V=8, k=9, tl=P, ti=P), UNSUPPORTED), (dict(k=4), INVALID), (dict(z=0), INVALID),
     (dict(t=0), INVALID), (dict(logp=0), INVALID), (dict(ent=0), INVALID),
     (dict(stats=P + 4), UNSUPPORTED), (dict(z=P + 1), UNSUPPORTED), (dict(t=P + 4), UNSUPPORTED),
