@@ -13,14 +13,15 @@
 // at -200, below which 2^t is 0 in fp32 (0 times -infinity would not be).
 //
 // The k best cost the pass next to nothing: each thread's running maximum is the
-// largest of its 1/256 of the row, at least k logits reach the k-th largest of
-// those maxima, and only the threads that reach it (k, without ties) hold such
-// logits.  The few of their vectors that hold any are read again (a thread
+// largest of its 1/256 of the row.  Where each of the 8 warps has k / 8 maxima
+// that reach a bound, at least k logits do, and only the threads that reach it
+// (21 on average with k up to 8, 54 with 32) hold such logits.  The few of their vectors that hold any are read again (a thread
 // leaves the maximum of every 4 vectors in shared memory), and what passes goes
 // to a list there as 64-bit keys (ordered value, then the lower index first),
 // which is cut to its k best.  Ties: where many threads reach the bound (rows of
-// equal logits, masks of one value with less than k tokens left), what is above
-// the bound is collected so and the equals are then taken from the row's
+// equal logits, masks of one value with less than k tokens left), the bound is
+// raised to the k-th largest of all maxima; where many reach that too, what is
+// above it is collected so and the equals are then taken from the row's
 // beginning until k are there; and a list that overflows (a row whose large
 // logits all sit in few threads' vectors) is collected in rounds over the whole
 // row, each cut before the next.
@@ -41,7 +42,7 @@ constexpr int LP_TILE = LP_NT * LP_U;  // vectors per CTA and tile
 constexpr int LP_MAX_K = 32;        // alternatives at most (one per lane)
 constexpr int LP_TRIG = 64;         // appended keys above k that make a cut worth it
 constexpr int LP_CAP = LP_NT * 8 + LP_MAX_K + LP_TRIG + 32;  // keys the list holds
-constexpr int LP_MAX_REACH = 64;    // threads that reach the bound: more are ties
+constexpr int LP_MAX_REACH = 96;    // threads that reach the bound: more are ties
 constexpr int LP_SLOTS = 32;        // maxima that a thread leaves
 
 struct LpFwdArgs {
@@ -218,6 +219,21 @@ __device__ __forceinline__ void lp_cut(LpTopSmem& s, int k) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = s.cnt;
   __syncthreads();  // everyone has read the count
+  if (c <= LP_NT) {  // a key's place is the number of larger ones
+    unsigned long long key = 0;
+    int place = 0;
+    if (threadIdx.x < c) {
+      key = s.buf[threadIdx.x];
+#pragma unroll 8
+      for (int i = 0; i < c; ++i) place += s.buf[i] > key;
+    }
+    __syncthreads();
+    if (threadIdx.x < c && place < 32) s.buf[place] = place < k ? key : 0ull;
+    if (threadIdx.x >= c && threadIdx.x < 32) s.buf[threadIdx.x] = 0ull;
+    if (threadIdx.x == 0) s.cnt = min(c, k);
+    __syncthreads();
+    return;
+  }
   unsigned long long best = 0;
   for (int b = warp * 32; b < c; b += LP_NT) {
     unsigned long long v = b + lane < c ? s.buf[b + lane] : 0ull;
@@ -288,9 +304,15 @@ struct LpPart {
     const uint32_t lo16 =
         lo == 0 ? 0u : lp_ord(__uint_as_float(__float_as_uint(lp_unord(lo)) & 0xFFFF0000u));
     if (own >= lo && own > 0) {
-      for (int q = 0; q << sh < tiles; ++q)
-        if (lp_ord(__uint_as_float(static_cast<uint32_t>(s.slot[q][tid]) << 16)) >= lo16)
-          s.item[atomicAdd(&s.items, 1)] = static_cast<uint16_t>(q * LP_NT + tid);
+      for (int q0 = 0; q0 << sh < tiles; q0 += 8) {
+        uint32_t m[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = static_cast<uint32_t>(s.slot[q0 + i][tid]) << 16;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if ((q0 + i) << sh < tiles && lp_ord(__uint_as_float(m[i])) >= lo16)
+            s.item[atomicAdd(&s.items, 1)] = static_cast<uint16_t>((q0 + i) * LP_NT + tid);
+      }
       if (tid < extra) append_one(s, tid, lo, false);
     }
     __syncthreads();
@@ -345,24 +367,40 @@ struct LpPart {
   // thread's largest logit (0: it has none).
   __device__ void top(LpTopSmem& s, uint32_t own, int k) const {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // the k-th largest of the threads' largest: each warp's in order, then the
-    // 8 lists merged in pairs
-    uint32_t best = warp_sort_desc(own, lane);
+    // a bound that k maxima reach: each warp's ((k + 7) / 8)-th largest, the
+    // smallest of the 8
+    uint32_t rest = own, rth = 0;
+    for (int i = (k + 7) / 8; i > 0; --i) {
+      rth = __reduce_max_sync(0xffffffffu, rest);
+      if (lane == __ffs(__ballot_sync(0xffffffffu, rest == rth)) - 1) rest = 0;
+    }
     uint32_t(*part)[32] = reinterpret_cast<uint32_t(*)[32]>(s.part);
-    part[warp][lane] = best;
+    if (lane == 0) part[0][warp] = rth;
     if (tid == 0) s.cnt = s.items = 0;
     __syncthreads();
+    uint32_t lo = part[0][0];
 #pragma unroll
-    for (int n = LP_NT / 64; n >= 1; n >>= 1) {
-      if (warp < n) {
-        best = warp_merge_desc(best, part[warp + n][31 - lane], lane);
-        part[warp][lane] = best;
-        if (n == 1 && lane == k - 1) s.bound = best;
-      }
+    for (int w = 1; w < LP_NT / 32; ++w) lo = min(lo, part[0][w]);
+    // (a bound of 0: a thread without logits, and so at most one slot a thread)
+    int reach = __syncthreads_count(own >= lo && own > 0);
+    if (reach > LP_MAX_REACH && lo != 0) {
+      // the k-th largest of all maxima: each warp's in order, then the 8 lists
+      // merged in pairs
+      uint32_t best = warp_sort_desc(own, lane);
+      part[warp][lane] = best;
       __syncthreads();
+#pragma unroll
+      for (int n = LP_NT / 64; n >= 1; n >>= 1) {
+        if (warp < n) {
+          best = warp_merge_desc(best, part[warp + n][31 - lane], lane);
+          part[warp][lane] = best;
+          if (n == 1 && lane == k - 1) s.bound = best;
+        }
+        __syncthreads();
+      }
+      lo = s.bound;
+      reach = __syncthreads_count(own >= lo && own > 0);
     }
-    const uint32_t lo = s.bound;
-    const int reach = __syncthreads_count(own >= lo && own > 0);
     if (reach <= LP_MAX_REACH || lo == 0) {
       const int n = collect(s, own, lo);
       if (n <= LP_CAP) lp_cut(s, k);
