@@ -496,6 +496,7 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS) k_token_logprobs(const LpFwdAr
     }
   };
   fetch(p.v0);
+  const uint4* ahead = p.zv + p.v0 + LP_TILE + tid;  // this thread's first vector there
   const int shift = TOP ? p.slot_shift() : 0;
   int tile = 0;
   float slot_max = -INFINITY;
@@ -503,7 +504,13 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS) k_token_logprobs(const LpFwdAr
     uint4 raw[LP_U];
 #pragma unroll
     for (int u = 0; u < LP_U; ++u) raw[u] = next[u];
-    fetch(b + LP_TILE);
+    if (b + 2 * LP_TILE <= p.v1) {  // (whole tiles need no look at their end)
+#pragma unroll
+      for (int u = 0; u < LP_U; ++u) next[u] = ld_nc_v4(ahead + u * LP_NT);
+      ahead += LP_TILE;
+    } else {
+      fetch(b + LP_TILE);
+    }
     const float tm = VT::max4(raw);
     if constexpr (TOP) {
       slot_max = fmax_nan(slot_max, tm);
