@@ -8,7 +8,7 @@
 // buffer, and added with its scales into fp32 registers.  Rows, columns and
 // the end of K that the tiles overhang are zeros that TMA fills in.
 //
-//   k_fp8_pair    many tokens: 256 tokens x 256 weight rows per CTA pair
+//   k_fp8_pair    many tokens: 256 tokens x 256 (or 128) weight rows per CTA pair
 //                 (cta_group::2), a TMEM lane holds one token; bound by the
 //                 tensor cores' rate.
 //   k_fp8_skinny  few tokens: the weight's rows are the MMA's M side, 128 per
@@ -52,28 +52,35 @@ __device__ __forceinline__ __nv_bfloat16 fp8_out<__nv_bfloat16>(float v) {
 // ------------------------------------------------------------------ pairs
 // Roles of the 12 warps of each CTA: 0 TMA producer, 1 (which owns the TMEM) and
 // 2 the MMA issuers (even CTA), 4 .. 11 the two column halves of the four TMEM
-// lane quarters.  CTA r stages tokens [128 r, 128 r + 128) and weight rows [128 r,
-// 128 r + 128) of the tile, and holds its tokens' outputs.  Tiles go round the
-// pairs, tokens fastest, so that the pairs at work share weight tiles in L2.
-constexpr int P8_STAGES = 4;  // (6 measured the same)
-constexpr int P8_HALF = 128 * 128;  // bytes of tokens (or weight rows) per CTA and stage
-constexpr int P8_STAGE = 2 * P8_HALF;
+// lane quarters.  CTA r stages tokens [128 r, 128 r + 128) and weight rows
+// [BN / 2 r, BN / 2 (r + 1)) of the tile, and holds its tokens' outputs.  Tiles go
+// round the pairs, tokens fastest, so that the pairs at work share weight tiles in
+// L2.
+constexpr int P8_A = 128 * 128;  // bytes of tokens per CTA and stage
 constexpr int P8_THREADS = 384;
 constexpr int P8_EPI_WARPS = 8;
-constexpr int P8_ROW = 256;           // bytes of a row that are written at a time
-constexpr int P8_BOXES = P8_ROW / 128;
-constexpr int P8_OUT = P8_ROW + 16;   // a lane's shared memory: a copy may start inside a unit
-constexpr int P8_SMEM = P8_STAGES * P8_STAGE + P8_EPI_WARPS * 32 * P8_OUT + 256 + 1024;
+constexpr int P8_ROW = 256;          // bytes of a row that are written at a time, at most
+constexpr int P8_OUT = P8_ROW + 16;  // a lane's shared memory: a copy may start inside a unit
+
+template <int BN>
+struct P8 {
+  static constexpr int B = BN / 2 * 128;  // bytes of weight rows per CTA and stage
+  static constexpr int STAGE = P8_A + B;
+  static constexpr int STAGES = BN == 256 ? 4 : 6;  // (256: 6 measured the same)
+  static constexpr int BUFS = 512 / BN;  // TMEM buffers
+  static constexpr int HN = BN / 2;      // columns of an epilogue warp
+  static constexpr int SMEM = STAGES * STAGE + P8_EPI_WARPS * 32 * P8_OUT + 256 + 1024;
+};
 
 // A warp's outputs leave through its shared memory, by copies that run while the
 // next tile is computed.  (A lane that stored its row itself would touch 32 lines
 // an instruction; rows written by whole warps cost more instructions than the
 // tile's additions when N is odd.)
 //
-// Where D's rows start on 16-byte boundaries: PIECES boxes of 32 rows x 128
+// Where D's rows start on 16-byte boundaries: BOXES boxes of 32 rows x 128
 // bytes, a row's 16-byte units permuted by the row as TMA's 128-byte swizzle has
 // them.  Called by all lanes (lane = row); v holds the lane's outputs.
-template <typename TO>
+template <typename TO, int BOXES>
 __device__ __forceinline__ void p8_write_boxes(const CUtensorMap* map, const Fp8Gemm& g,
                                                uint8_t* buf, const float* v, int row0, int col,
                                                int lane) {
@@ -81,7 +88,7 @@ __device__ __forceinline__ void p8_write_boxes(const CUtensorMap* map, const Fp8
   if (lane == 0) bulk_wait_read();  // the last copies have left the buffer
   __syncwarp();
 #pragma unroll
-  for (int q = 0; q < P8_BOXES; ++q) {
+  for (int q = 0; q < BOXES; ++q) {
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const float* x = v + q * COLS + u * (COLS / 8);
@@ -99,19 +106,18 @@ __device__ __forceinline__ void p8_write_boxes(const CUtensorMap* map, const Fp8
   __syncwarp();
   if (lane == 0) {
 #pragma unroll
-    for (int q = 0; q < P8_BOXES; ++q)
+    for (int q = 0; q < BOXES; ++q)
       if (col + q * COLS < g.N) tma_store_2d(map, buf + q * 4096, col + q * COLS, row0);
     bulk_commit();
   }
 }
 
-// Elsewhere: `count` consecutive outputs of one row, v, to d.  The lane puts them
+// Elsewhere: `count` consecutive outputs of one row (W words at most), v, to d.  The lane puts them
 // into its own piece of shared memory, at the place in a 16-byte unit that they
 // have in D, and hands the whole units to one copy; what fills no unit is stored
 // directly.
-template <typename TO>
+template <typename TO, int W>
 __device__ __forceinline__ void p8_write_row(TO* d, uint8_t* buf, const float* v, int count) {
-  constexpr int W = P8_ROW / 4;
   uint32_t w[W];
 #pragma unroll
   for (int i = 0; i < W; ++i) {
@@ -168,20 +174,21 @@ __device__ __forceinline__ void p8_write_row(TO* d, uint8_t* buf, const float* v
   }
 }
 
-template <typename TO>
+template <typename TO, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
     k_fp8_pair(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                const __grid_constant__ CUtensorMap mapD, const __grid_constant__ Fp8Gemm g) {
+  using C = P8<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* ring = smem;  // stage: tokens, then weight rows
-  uint8_t* outs = ring + P8_STAGES * P8_STAGE;
+  uint8_t* outs = ring + C::STAGES * C::STAGE;
   uint64_t* full = reinterpret_cast<uint64_t*>(outs + P8_EPI_WARPS * 32 * P8_OUT);  // even CTA's are used
-  uint64_t* empty = full + P8_STAGES;   // each CTA
-  uint64_t* tfull = empty + P8_STAGES;  // [2] each CTA
-  uint64_t* tempty = tfull + 2;         // [2] even CTA's are used
-  uint64_t* drain = tempty + 2;
+  uint64_t* empty = full + C::STAGES;   // each CTA
+  uint64_t* tfull = empty + C::STAGES;  // [BUFS] each CTA
+  uint64_t* tempty = tfull + C::BUFS;   // [BUFS] even CTA's are used
+  uint64_t* drain = tempty + C::BUFS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -192,11 +199,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
   const int tiles = g.m_tiles * g.n_tiles;  // (below 2^30: checked by the host)
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < P8_STAGES; ++s) {
+    for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < C::BUFS; ++a) {
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], 2 * P8_EPI_WARPS);
     }
@@ -227,19 +234,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
       bool ok = true;
       for (int t = pair; t < tiles && ok; t += pairs) {
         const int m0 = (t % g.m_tiles) * 256 + static_cast<int>(rank) * 128;
-        const int n0 = (t / g.m_tiles) * 256 + static_cast<int>(rank) * 128;
+        const int n0 = (t / g.m_tiles) * BN + static_cast<int>(rank) * C::HN;
         for (int kb = 0; kb < g.KB; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) {
             ok = false;
             break;
           }
           const uint32_t fbar = mapa_shared(smem_u32(&full[stage]), 0);
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * P8_STAGE);
-          uint8_t* dst = ring + stage * P8_STAGE;
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE);
+          uint8_t* dst = ring + stage * C::STAGE;
           tma_load_2d_pair(&mapA, fbar, dst, kb * 128, m0);
-          tma_load_2d_pair(&mapB, fbar, dst + P8_HALF, kb * 128, n0);
+          tma_load_2d_pair(&mapB, fbar, dst + P8_A, kb * 128, n0);
           ++issued;
-          if (++stage == P8_STAGES) {
+          if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1u;
           }
@@ -248,9 +255,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
       // every stage this CTA filled has been consumed before it leaves
       int s = stage;
       uint32_t ph = phase;
-      for (int i = 0; i < P8_STAGES && i < issued; ++i) {
+      for (int i = 0; i < C::STAGES && i < issued; ++i) {
         if (--s < 0) {
-          s = P8_STAGES - 1;
+          s = C::STAGES - 1;
           ph ^= 1u;
         }
         mbar_drain_wait(&empty[s], ph, g.wait_limit_ns);
@@ -258,40 +265,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
     } else if ((warp == 1 || warp == 2) && lane == 0 && leader) {
       // warp 1 the even blocks, warp 2 the odd: their buffers differ, so nothing
       // orders the two, and the waits of one pass while the other's MMAs run
-      constexpr uint32_t idesc = idesc_e4m3_f32(256, 256);
+      constexpr uint32_t idesc = idesc_e4m3_f32(256, BN);
       const uint64_t d0 = smem_desc_sw128(0, 16u, 1024u);
       const uint64_t hi = d0 & ~uint64_t(0xFFFFFFFFu);
       const uint32_t r0 = static_cast<uint32_t>(d0) + ((smem_u32(ring) & 0x3FFFFu) >> 4);
-      const uint32_t buf = warp - 1;
+      uint32_t buf = warp - 1;
       const long long total =
           static_cast<long long>((tiles - pair + pairs - 1) / pairs) * g.KB;  // of this pair
-      int stage = buf;
+      int stage = warp - 1;
       uint32_t phase = 0, tphase = 1;
-      for (long long it = buf; it < total; it += 2) {
+      for (long long it = warp - 1; it < total; it += 2) {
         if (!mbar_wait(&full[stage], phase, wc) || !mbar_wait(&tempty[buf], tphase, wc)) break;
         tc_fence_after();
-        const uint32_t a = r0 + stage * (P8_STAGE >> 4);
+        const uint32_t a = r0 + stage * (C::STAGE >> 4);
 #pragma unroll
         for (uint32_t k = 0; k < 4; ++k)
-          tc_mma_pair_f8(tmem + buf * 256, hi | (a + 2 * k), hi | (a + (P8_HALF >> 4) + 2 * k),
+          tc_mma_pair_f8(tmem + buf * BN, hi | (a + 2 * k), hi | (a + (P8_A >> 4) + 2 * k),
                          idesc, k);
         tc_commit_pair(&tfull[buf], 0x3);
         tc_commit_pair(&empty[stage], 0x3);
-        tphase ^= 1u;
+        buf += 2;
+        if (buf >= C::BUFS) {
+          buf -= C::BUFS;
+          tphase ^= 1u;
+        }
         stage += 2;
-        if (stage >= P8_STAGES) {
-          stage -= P8_STAGES;
+        if (stage >= C::STAGES) {
+          stage -= C::STAGES;
           phase ^= 1u;
         }
       }
-      tc_commit_pair(&drain[buf], 0x1);
-      mbar_drain_wait(&drain[buf], 0, g.wait_limit_ns);
+      tc_commit_pair(&drain[warp - 1], 0x1);
+      mbar_drain_wait(&drain[warp - 1], 0, g.wait_limit_ns);
     }
     __syncwarp();
   } else {
     reg_alloc<224>();
     const int quad = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * C::HN;
     const uint32_t tempty0 = mapa_shared(smem_u32(tempty), 0);
     const int nb_last = (g.N - 1) / 128;
     // (boxes start on 1024-byte boundaries, a lane's rows on 16-byte ones)
@@ -308,9 +319,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
     auto place = [&](int t) {
       const int nt = t / g.m_tiles, mt = t - nt * g.m_tiles;
       row0 = mt * 256 + static_cast<int>(rank) * 128 + quad * 32;
-      col0 = nt * 256 + half * 128;
+      col0 = nt * BN + half * C::HN;
       pa = g.sa + static_cast<size_t>(min(row0 + lane, g.M - 1)) * g.KB;
-      pb = g.sb + static_cast<size_t>(min(nt * 2 + half, nb_last)) * g.KB;
+      pb = g.sb + static_cast<size_t>(min(col0 / 128, nb_last)) * g.KB;
     };
     float4 na, nb;
     auto load4 = [&](int kb) {
@@ -329,9 +340,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
       load4(0);
     }
     for (int t = pair; t < tiles && ok; t += pairs) {
-      float acc[128];
+      float acc[C::HN];
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      for (int i = 0; i < C::HN; ++i) acc[i] = 0.f;
       const int out_row = row0, out_col = col0;
       for (int k4 = 0; k4 < g.KB && ok; k4 += 4) {
         const float s4[4] = {na.x * nb.x, na.y * nb.y, na.z * nb.z, na.w * nb.w};
@@ -344,20 +355,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (k4 + j >= g.KB) break;
-          const uint32_t buf = it & 1;
-          ok = mbar_wait(&tfull[buf], (it >> 1) & 1, wc);
+          const uint32_t buf = it % C::BUFS;
+          ok = mbar_wait(&tfull[buf], (it / C::BUFS) & 1, wc);
           if (!__all_sync(0xffffffffu, ok)) {
             ok = false;
             break;
           }
           tc_fence_after();
           uint32_t r[2][16];  // one piece on its way while the other is added
-          tmem_ld16_async(tl + buf * 256, r[0]);
+          tmem_ld16_async(tl + buf * BN, r[0]);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
+          for (int c = 0; c < C::HN / 16; ++c) {
             tmem_wait16(r[c & 1]);
-            if (c < 7) {
-              tmem_ld16_async(tl + buf * 256 + (c + 1) * 16, r[(c + 1) & 1]);
+            if (c + 1 < C::HN / 16) {
+              tmem_ld16_async(tl + buf * BN + (c + 1) * 16, r[(c + 1) & 1]);
             } else {
               // the buffer is read: the MMAs may have it back
               tc_fence_before();
@@ -372,23 +383,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
           ++it;
         }
       }
-      const int cols = min(128, g.N - out_col);
+      const int cols = min(C::HN, g.N - out_col);
       if (ok && out_row < g.M && cols > 0) {
         if (g.bias != nullptr) {
           const TO* b = static_cast<const TO*>(g.bias) + out_col;
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
+          for (int i = 0; i < C::HN; ++i)
             if (i < cols) acc[i] += static_cast<float>(b[i]);
         }
-        constexpr int COLS = P8_ROW / sizeof(TO);
+        constexpr int E = static_cast<int>(sizeof(TO));
+        constexpr int COLS = P8_ROW / E < C::HN ? P8_ROW / E : C::HN;
         TO* d = static_cast<TO*>(g.D) + static_cast<size_t>(out_row + lane) * g.N + out_col;
 #pragma unroll
-        for (int c = 0; c < 128 / COLS; ++c) {
+        for (int c = 0; c < C::HN / COLS; ++c) {
           if (c * COLS >= cols) break;
           if (g.vec)
-            p8_write_boxes<TO>(&mapD, g, out, acc + c * COLS, out_row, out_col + c * COLS, lane);
+            p8_write_boxes<TO, COLS * E / 128>(&mapD, g, out, acc + c * COLS, out_row,
+                                               out_col + c * COLS, lane);
           else if (out_row + lane < g.M)
-            p8_write_row<TO>(d + c * COLS, out, acc + c * COLS, min(COLS, cols - c * COLS));
+            p8_write_row<TO, COLS * E / 4>(d + c * COLS, out, acc + c * COLS,
+                                           min(COLS, cols - c * COLS));
         }
       }
       __syncwarp();

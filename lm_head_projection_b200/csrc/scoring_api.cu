@@ -140,23 +140,23 @@ struct Fp8Call {
   cudaStream_t st;
 };
 
-template <typename TO>
+template <typename TO, int BN>
 flkl_status launch_pair(const Fp8Call& c) {
   static bool done[kMaxDevices];
-  if (!raise_smem(k_fp8_pair<TO>, done)) return FLKL_ERR_CUDA;
+  if (!raise_smem(k_fp8_pair<TO, BN>, done)) return FLKL_ERR_CUDA;
   Fp8Gemm g = c.g;
   g.m_tiles = (g.M - 1) / 256 + 1;
-  g.n_tiles = (g.N - 1) / 256 + 1;
+  g.n_tiles = (g.N - 1) / BN + 1;
   g.vec = (size_t(g.N) * sizeof(TO)) % 16 == 0 && aligned(g.D, 16);
   const int64_t tiles = int64_t(g.m_tiles) * g.n_tiles;
   if (tiles >= (int64_t(1) << 30)) return FLKL_ERR_UNSUPPORTED;
   CUtensorMap ma, mb, md;
-  if (!fp8_map(&ma, c.A, c.K, g.M, 128) || !fp8_map(&mb, c.B, c.K, g.N, 128))
+  if (!fp8_map(&ma, c.A, c.K, g.M, 128) || !fp8_map(&mb, c.B, c.K, g.N, BN / 2))
     return FLKL_ERR_CUDA;
   md = ma;  // (not used where the rows of D are not on 16-byte boundaries)
   if (g.vec && !out_map<TO>(&md, g.D, g.M, g.N)) return FLKL_ERR_CUDA;
   const int pairs = static_cast<int>(std::min<int64_t>(resident_clusters(2), tiles));
-  k_fp8_pair<TO><<<2 * pairs, P8_THREADS, P8_SMEM, c.st>>>(ma, mb, md, g);
+  k_fp8_pair<TO, BN><<<2 * pairs, P8_THREADS, P8<BN>::SMEM, c.st>>>(ma, mb, md, g);
   return launched();
 }
 
@@ -190,17 +190,16 @@ flkl_status launch_skinny(const Fp8Call& c, int cluster) {
                                                                                  : FLKL_ERR_CUDA;
 }
 
-// Which kernel.  A pair's 256 x 256 tile holds 8 of the small kernel's 128 x 64
-// tiles on two SMs and takes about as long per block of K, so that it wins where
-// a quarter of the pairs have a tile: 128 x 14336 x 4096 takes them 24 us (one
-// tile of 128 tokens in the small kernel: 30), 129 x 1000 x 8192 36 us (18).  Up
-// to 64 rows there is one token tile and the weight is streamed at HBM's rate
-// (64 x 128256 x 4096: 104 us, pairs 133).
+// Which kernel.  Up to 64 rows there is one token tile and the weight is streamed
+// at HBM's rate (64 x 128256 x 4096: 104 us, pairs 133).  Beyond, the pairs' tiles
+// hold 4 or 8 of the small kernel's 128 x 64 ones on two SMs and take about as long
+// per block of K: they win from a dozen large tiles on (256 x 4096 x 4096, 16
+// tiles: 18.8 against 23.5 us; 129 x 1000 x 8192, 4 tiles: 36 against 18 us).
 template <typename TO>
 flkl_status fp8_matmul(const Fp8Call& c) {
   const int M = c.g.M, KB = c.g.KB, sms = device_sms();
   const int64_t pair_tiles = int64_t((M - 1) / 256 + 1) * ((c.g.N - 1) / 256 + 1);
-  if (M <= 64 || pair_tiles <= sms / 8) {
+  if (M <= 64 || pair_tiles <= sms / 12) {
     // CTAs that share a tile, each with a part of K: as many as run at once
     const int64_t tiles = int64_t((c.g.N - 1) / 128 + 1) * ((M - 1) / 64 + 1);
     int cluster = static_cast<int>(std::min<int64_t>({S8_MAX_CLUSTER, sms / tiles, KB}));
@@ -214,7 +213,11 @@ flkl_status fp8_matmul(const Fp8Call& c) {
       return launch_skinny<TO, 64>(c, cluster);
     }
   }
-  return launch_pair<TO>(c);
+  // Tiles of 128 weight rows where they all run at once: a wave of them takes 0.7
+  // of the larger ones' (300 x 4096 x 4096: 18.8 against 24.2 us; two waves of them
+  // against one lose: 777 x 4096 x 4096 28.7 against 24.6).
+  if (pair_tiles <= resident_clusters(2) / 2) return launch_pair<TO, 128>(c);
+  return launch_pair<TO, 256>(c);
 }
 
 // --------------------------------------------------------- log-probabilities

@@ -256,6 +256,25 @@ def test_block_matmul_output_at_any_place(out, N):
             assert (buf[:off] == 7).all() and (buf[off + M * N:] == 7).all()
 
 
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K", [
+    (300, 2600, 272), (300, 2601, 1040), (257, 4607, 16), (512, 4352, 656),   # 128-wide tiles
+    (520, 3303, 272), (1000, 2504, 1040), (300, 5001, 144), (769, 2900, 16)])  # 256-wide
+def test_block_matmul_of_cta_pairs(M, N, K, out):
+    """Both tile widths of the pairs: rows of any phase, ends inside tiles, several
+    tiles a pair, a bias; nothing beside D is touched."""
+    from lm_head_projection_b200 import fp8
+
+    qa, sa, qb, sb, want = _product(M, N, K, out, False)
+    _product(M, N, K, out, True)
+    for off in (0, 3):
+        buf = torch.full((M * N + 24,), 7.0, dtype=DT[out], device="cuda")
+        d = buf[off:off + M * N].view(M, N)
+        fp8.block_matmul(qa, sa, qb, sb, out_dtype=DT[out], out=d)
+        assert torch.equal(d, want)
+        assert (buf[:off] == 7).all() and (buf[off + M * N:] == 7).all()
+
+
 @pytest.mark.parametrize("M", [3, 130])
 def test_block_matmul_rows_do_not_depend_on_the_batch(M):
     """Twice the same, and (within one kernel's range of M) a row's result does
