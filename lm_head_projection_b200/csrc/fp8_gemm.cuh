@@ -17,6 +17,22 @@
 //                 bound by HBM.  Also more tokens, in tiles of 64, where the
 //                 pairs' tiles would leave most SMs idle.
 //
+// What bounds the pairs: a 256 x 256 block is 512 clocks of MMAs, 256 of TMEM reads
+// and 256 of additions per SM quarter, which would fit side by side; but a buffer's
+// way round (commit, wake, read, arrival in the other CTA, wake: about 700 clocks
+// beside the 450 of the read) has only two buffers to hide behind, as 512 columns
+// of TMEM hold no third.  1024 x 128256 x 4096 takes 857 clocks a block (635 without
+// additions and stores) and 507 us (2120 TFLOP/s) in a burst; back to back the
+// power limit holds the clock at 1.3 - 1.5 GHz (578 us).  What made it so: two issuing
+// threads instead of one (585 -> 551 us), reads of 16 columns with the next on its
+// way (551 -> 528), a relaxed arrival (a cluster-scope release cost 1100 clocks a
+// block), the scales of four blocks in one load.  Measured and left: tokens on the
+// N side (their scales then come from shared memory, 512 bytes a load: 892 us),
+// 16 epilogue warps, two MMAs of half the width, packed additions, a deeper ring.
+//
+// The small kernel: 1 x 128256 x 4096 92 us (525 MB, 5.7 TB/s; 1002 tiles on 148
+// SMs are 6.8 waves, the last one short); 40 x 4096 x 4096 about 6 us on the device.
+//
 // Every wait is bounded; on a timeout the CTA stops computing, lets its copies
 // and MMAs land, frees TMEM and returns, and the status word says so.
 #pragma once
@@ -184,7 +200,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* ring = smem;  // stage: tokens, then weight rows
   uint8_t* outs = ring + C::STAGES * C::STAGE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(outs + P8_EPI_WARPS * 32 * P8_OUT);  // even CTA's are used
+  // even CTA's are used
+  uint64_t* full = reinterpret_cast<uint64_t*>(outs + P8_EPI_WARPS * 32 * P8_OUT);
   uint64_t* empty = full + C::STAGES;   // each CTA
   uint64_t* tfull = empty + C::STAGES;  // [BUFS] each CTA
   uint64_t* tempty = tfull + C::BUFS;   // [BUFS] even CTA's are used

@@ -1,4 +1,4 @@
-// Host side of the norm-backward entry points declared in include/flkl.h.
+// Host side of the norm entry points declared in include/flkl.h.
 
 #include <algorithm>
 #include <mutex>

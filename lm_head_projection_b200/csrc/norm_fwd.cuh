@@ -11,7 +11,11 @@
 // HBM-bound (bf16 in, e4m3 out: 7 bytes per element and nothing to reuse), so a
 // row is read once into registers, 8 columns per thread and vector, and every
 // output leaves from there.  A row of at most 256 columns is one warp's (4 rows
-// per CTA, no barrier); wider rows are one CTA's.
+// per CTA, no barrier); wider rows are one CTA's.  Measured: 8192 x 8192 bf16 to
+// e4m3 79 us (470 MB, 5.9 TB/s; a copy reaches 6.5), to bf16 84 us (6.4 TB/s);
+// 512 threads x 2 vectors took 88 us for what 256 x 4 did in 98 and 1024 x 1 in
+// 108, and a register limit that lets 2048 threads stand on an SM brought it to 79
+// (bf16; fp32 rows, whose loads are twice as wide, run best without).
 #pragma once
 
 #include "fp8.cuh"
@@ -33,7 +37,8 @@ struct NormFwdArgs {
 // G threads per row, VPT vectors of 8 columns per thread (H <= 8 G VPT);
 // NT threads per CTA, NT / G rows.
 template <typename T, int NT, int G, int VPT, bool QUANT>
-__global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 2048 / NT : 1) k_add_rms_norm(const NormFwdArgs a) {
+__global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 2048 / NT : 1)
+    k_add_rms_norm(const NormFwdArgs a) {
   constexpr int NW = G / 32;
   __shared__ float red[NW > 1 ? NW : 1];
   const int lane = threadIdx.x & 31;

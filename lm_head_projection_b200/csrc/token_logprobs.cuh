@@ -15,20 +15,29 @@
 // The k best cost the pass next to nothing: each thread's running maximum is the
 // largest of its 1/256 of the row.  Where each of the 8 warps has k / 8 maxima
 // that reach a bound, at least k logits do, and only the threads that reach it
-// (21 on average with k up to 8, 54 with 32) hold such logits.  The few of their vectors that hold any are read again (a thread
-// leaves the maximum of every 4 vectors in shared memory), and what passes goes
-// to a list there as 64-bit keys (ordered value, then the lower index first),
-// which is cut to its k best.  Ties: where many threads reach the bound (rows of
-// equal logits, masks of one value with less than k tokens left), the bound is
-// raised to the k-th largest of all maxima; where many reach that too, what is
-// above it is collected so and the equals are then taken from the row's
-// beginning until k are there; and a list that overflows (a row whose large
-// logits all sit in few threads' vectors) is collected in rounds over the whole
-// row, each cut before the next.
+// (21 on average with k up to 8, 54 with 32) hold such logits.  The few of their
+// vectors that hold any are read again (a thread leaves the maximum of every 4
+// vectors in shared memory), and what passes goes to a list there as 64-bit keys
+// (ordered value, then the lower index first), which is cut to its k best.
+//
+// Ties: where many threads reach the bound (rows of equal logits, masks of one
+// value with less than k tokens left), the bound is raised to the k-th largest of
+// all maxima; where many reach that too, what is above it is collected so and the
+// equals are then taken from the row's beginning until k are there; and a list
+// that overflows (a row whose large logits all sit in few threads' vectors) is
+// collected in rounds over the whole row, each cut before the next.
 //
 // One CTA per row; rows that are too few to fill the machine are split over a
 // cluster of 2, 4 or 8 CTAs, which leave their sums and k best in shared memory
 // for the first to join, in rank order.
+//
+// Bound by instruction issue and HBM together: an exponential takes 8 clocks of an
+// SM quarter per 32 logits, the rest of a bf16 logit about 7 issue slots (two
+// logits an instruction where there is one).  Measured, 2048 x 128256 bf16 (525 MB):
+// 92 us without alternatives (5.7 TB/s), 106 us with 5, 112 us with 32; 1024 x
+// 128256 fp32: 79 and 91 us (6.6 and 5.8 TB/s).  Four CTAs of 256 threads an SM with
+// the next tile on its way beat five without (97 against 103 us); the alternatives
+// as a running list in the pass, cut as it grew, took 286 us.
 #pragma once
 
 #include "ptx.cuh"
@@ -93,7 +102,9 @@ struct LpVec;
 template <>
 struct LpVec<__nv_bfloat16> {
   static constexpr int E = 8;
-  __device__ static uint4 empty() { return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
+  __device__ static uint4 empty() {  // of -infinity
+    return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+  }
   __device__ static void unpack(const uint4& u, float (&f)[8]) { unpack8_bf16(u, f); }
   __device__ static float max(const uint4& u) {
     uint32_t a, b, c;
@@ -130,7 +141,9 @@ struct LpVec<__nv_bfloat16> {
 template <>
 struct LpVec<float> {
   static constexpr int E = 4;
-  __device__ static uint4 empty() { return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u); }
+  __device__ static uint4 empty() {
+    return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+  }
   __device__ static void unpack(const uint4& u, float (&f)[4]) {
     f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
     f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);

@@ -14,6 +14,7 @@ from __future__ import annotations
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (DTYPES, _check_dev, _launch, _ptr, flkl_token_logprobs_backward,
                flkl_token_logprobs_forward)
@@ -135,6 +136,7 @@ class _TokenLogProbsFunction(torch.autograd.Function):
         return r["logp"], r["entropy"], r["top_logp"], r["top_ids"]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dlogp, dentropy, dtop, _ids):
         logits, target, stats, entropy, top_ids = ctx.saved_tensors
         ignore_index, temperature = ctx.opts

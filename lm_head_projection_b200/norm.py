@@ -22,6 +22,7 @@ from __future__ import annotations
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (DTYPES, FLKL_OK, FlklError, _check_dev, _launch, _ptr,
                flkl_add_rms_norm_backward, flkl_add_rms_norm_forward, flkl_layer_norm_backward,
@@ -160,6 +161,7 @@ class _AddRMSNormFunction(torch.autograd.Function):
         return r["Y"], r["H"]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY, dH):
         H, W = ctx.saved_tensors
         if dY is None:

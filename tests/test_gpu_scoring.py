@@ -568,6 +568,22 @@ def test_token_logprobs_autograd():
         assert abs(num - float(buf.grad[0, c])) < 2e-3 * max(1e-2, abs(num)) + 1e-4
 
 
+def test_second_gradients_are_refused():
+    from lm_head_projection_b200.logprobs import token_logprobs
+    from lm_head_projection_b200.norm import AddRMSNorm
+
+    z, t = _logits(3, 50, "fp32")
+    z.requires_grad_()
+    g, = torch.autograd.grad(token_logprobs(z, t).logp.pow(2).sum(), z, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+    m = AddRMSNorm(64, dtype=torch.float32, device="cuda")
+    x, r, _ = [v.cuda().requires_grad_() for v in _norm_inputs(3, 64, "fp32")]
+    g, = torch.autograd.grad(m(x, r)[0].pow(2).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+
+
 # ------------------------------------------------- streams, graphs, the chain
 def _chain():
     from lm_head_projection_b200.fp8 import Fp8Head
