@@ -462,6 +462,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _check_dev(name, t, dtype, shape, device):
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
@@ -472,18 +474,18 @@ def _check_dev(name, t, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _launch(what: str, call, args, dev) -> None:
-    """``call(*args, stream)`` on the current stream of ``dev``, with ``dev`` as
-    the current device, since the library launches there; raises FlklError on a
-    non-OK status.  (Callers that are given a stream make it the current one
-    first, so that what they allocate belongs to it.)"""
+def _launch(what: str, dev, *args) -> None:
+    """The library's ``what(*args, stream)`` on the current stream of ``dev``, with
+    ``dev`` as the current device, since the library launches there; raises
+    FlklError on a non-OK status.  (Callers that are given a stream make it the
+    current one first, so that what they allocate belongs to it.)"""
     if dev.type != "cuda":
         raise ValueError(f"{what} needs CUDA tensors, got {dev}")
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _launch(what, call, args, dev)
+            return _launch(what, dev, *args)
     # (the raw handle: a Stream object costs as much as a small launch)
-    status = call(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    status = getattr(_lib(), what)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     if status != FLKL_OK:
         raise FlklError(status, what)
 

@@ -14,7 +14,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import DTYPES, _check_dev, _launch, _ptr, flkl_fp8_block_matmul, flkl_fp8_quantize
+from . import DTYPES, _check_dev, _launch, _ptr
 
 __all__ = ["quantize_rows", "quantize_blocks", "block_matmul", "Fp8Head"]
 
@@ -36,9 +36,8 @@ def _quantize(x: torch.Tensor, block_rows: int, stream) -> Tuple[torch.Tensor, t
     kb = -(-K // 128)
     shape = (*x.shape[:-1], kb) if block_rows == 1 else (-(-rows // 128), kb)
     scale = x.new_empty(shape, dtype=torch.float32)
-    _launch("flkl_fp8_quantize", flkl_fp8_quantize,
-            (x.data_ptr(), rows, K, DTYPES[x.dtype], block_rows, q.data_ptr(), scale.data_ptr()),
-            x.device)
+    _launch("flkl_fp8_quantize", x.device, x.data_ptr(), rows, K, DTYPES[x.dtype], block_rows,
+            q.data_ptr(), scale.data_ptr())
     return q, scale
 
 
@@ -85,9 +84,8 @@ def block_matmul(A: torch.Tensor, a_scale: torch.Tensor, B: torch.Tensor, b_scal
         out = A.new_empty((M, N), dtype=out_dtype)
     else:
         _check_dev("out", out, out_dtype, (M, N), dev)
-    _launch("flkl_fp8_block_matmul", flkl_fp8_block_matmul,
-            (A.data_ptr(), a_scale.data_ptr(), B.data_ptr(), b_scale.data_ptr(), _ptr(bias), M,
-             N, K, DTYPES[out_dtype], out.data_ptr()), dev)
+    _launch("flkl_fp8_block_matmul", dev, A.data_ptr(), a_scale.data_ptr(), B.data_ptr(),
+            b_scale.data_ptr(), _ptr(bias), M, N, K, DTYPES[out_dtype], out.data_ptr())
     return out
 
 

@@ -16,8 +16,7 @@ from typing import NamedTuple, Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (DTYPES, _check_dev, _launch, _ptr, flkl_token_logprobs_backward,
-               flkl_token_logprobs_forward)
+from . import DTYPES, _check_dev, _launch, _ptr
 
 __all__ = ["token_logprobs_forward", "token_logprobs_backward", "token_logprobs",
            "TokenLogProbs", "TokenLogProbsOutput", "MAX_TOP_K"]
@@ -68,10 +67,10 @@ def token_logprobs_forward(logits: torch.Tensor, target: Optional[torch.Tensor] 
     logp = torch.empty_like(entropy) if target is not None else None
     top_logp = entropy.new_empty((rows, top_k)) if top_k else None
     top_ids = logits.new_empty((rows, top_k), dtype=torch.int64) if top_k else None
-    _launch("flkl_token_logprobs_forward", flkl_token_logprobs_forward,
-            (logits.data_ptr(), ld, _ptr(target), ignore_index, rows, V, DTYPES[logits.dtype],
-             temperature, top_k, _ptr(logp), entropy.data_ptr(), lse.data_ptr(),
-             stats.data_ptr(), _ptr(top_logp), _ptr(top_ids)), dev)
+    _launch("flkl_token_logprobs_forward", dev, logits.data_ptr(), ld, _ptr(target),
+            ignore_index, rows, V, DTYPES[logits.dtype], temperature, top_k, _ptr(logp),
+            entropy.data_ptr(), lse.data_ptr(), stats.data_ptr(), _ptr(top_logp),
+            _ptr(top_ids))
     return {"logp": logp, "entropy": entropy, "lse": lse, "top_logp": top_logp,
             "top_ids": top_ids, "stats": stats}
 
@@ -109,10 +108,10 @@ def token_logprobs_backward(logits: torch.Tensor, target: Optional[torch.Tensor]
             raise ValueError("dtop_logp needs alternatives (top_k > 0)")
         _check_dev("dtop_logp", dtop_logp, f32, (rows, k), dev)
     dlogits = logits.new_empty_strided((rows, V), (ld, 1))
-    _launch("flkl_token_logprobs_backward", flkl_token_logprobs_backward,
-            (logits.data_ptr(), ld, _ptr(target), ignore_index, rows, V, DTYPES[logits.dtype],
-             temperature, k, stats.data_ptr(), entropy.data_ptr(), _ptr(top_ids), _ptr(dlogp),
-             _ptr(dentropy), _ptr(dtop_logp), dlogits.data_ptr(), ld), dev)
+    _launch("flkl_token_logprobs_backward", dev, logits.data_ptr(), ld, _ptr(target),
+            ignore_index, rows, V, DTYPES[logits.dtype], temperature, k, stats.data_ptr(),
+            entropy.data_ptr(), _ptr(top_ids), _ptr(dlogp), _ptr(dentropy), _ptr(dtop_logp),
+            dlogits.data_ptr(), ld)
     return dlogits
 
 

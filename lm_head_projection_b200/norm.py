@@ -24,8 +24,7 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (DTYPES, FLKL_OK, FlklError, _check_dev, _launch, _ptr,
-               flkl_add_rms_norm_backward, flkl_add_rms_norm_forward, flkl_layer_norm_backward,
+from . import (DTYPES, FLKL_OK, FlklError, _check_dev, _launch, _ptr, flkl_layer_norm_backward,
                flkl_norm_workspace_size, flkl_rms_norm_backward)
 
 __all__ = ["rms_norm_backward", "layer_norm_backward", "RMSNorm", "LayerNorm", "add_rms_norm",
@@ -118,9 +117,8 @@ def add_rms_norm(X: torch.Tensor, W: torch.Tensor, residual: Optional[torch.Tens
         raise ValueError("inplace needs a residual")
     Y = torch.empty_like(X, dtype=torch.float8_e4m3fn if quantize else dt)
     scale = X.new_empty((*X.shape[:-1], -(-H // 128)), dtype=torch.float32) if quantize else None
-    _launch("flkl_add_rms_norm_forward", flkl_add_rms_norm_forward,
-            (X.data_ptr(), _ptr(residual), W.data_ptr(), rows, H, DTYPES[dt], eps,
-             int(bool(quantize)), Y.data_ptr(), _ptr(scale), _ptr(Hs)), dev)
+    _launch("flkl_add_rms_norm_forward", dev, X.data_ptr(), _ptr(residual), W.data_ptr(), rows,
+            H, DTYPES[dt], eps, 1 if quantize else 0, Y.data_ptr(), _ptr(scale), _ptr(Hs))
     return {"Y": Y, "scale": scale, "H": X if Hs is None else Hs}
 
 
@@ -145,9 +143,9 @@ def add_rms_norm_backward(dY: torch.Tensor, H: torch.Tensor, W: torch.Tensor,
     else:
         need = flkl_norm_workspace_size(rows, hidden, compute_dW, False)
     ws = H.new_empty(need, dtype=torch.uint8) if need else None
-    _launch("flkl_add_rms_norm_backward", flkl_add_rms_norm_backward,
-            (_ptr(dY), _ptr(dH), _ptr(H), _ptr(W), rows, hidden, DTYPES[dt], eps, compute_dW,
-             accum_fp32, _ptr(dX), _ptr(dW), _ptr(ws), need), dev)
+    _launch("flkl_add_rms_norm_backward", dev, dY.data_ptr(), _ptr(dH), H.data_ptr(),
+            W.data_ptr(), rows, hidden, DTYPES[dt], eps, 1 if compute_dW else 0,
+            1 if accum_fp32 else 0, dX.data_ptr(), _ptr(dW), _ptr(ws), need)
     return {"dX": dX, "dW": dW}
 
 
