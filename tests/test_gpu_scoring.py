@@ -275,6 +275,34 @@ def test_block_matmul_of_cta_pairs(M, N, K, out):
         assert (buf[:off] == 7).all() and (buf[off + M * N:] == 7).all()
 
 
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("M,N,K", [(3400, 1, 272), (3600, 8, 144), (4100, 40, 16), (3333, 67, 144)])
+def test_block_matmul_of_many_rows_and_few_columns(M, N, K, out):
+    """Outputs narrower than a tile, a box and a 16-byte unit."""
+    _product(M, N, K, out, False)
+    _product(M, N, K, out, True)
+
+
+def test_block_matmul_too_deep_for_the_small_kernel():
+    """So deep that the tokens' scales leave no room for its ring: sampled columns
+    against fp64."""
+    from lm_head_projection_b200 import fp8
+
+    M, N, K = 3, 9601, 67216
+    g = torch.Generator(device="cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g)
+    qa, sa = fp8.quantize_rows(r(M, K))
+    qb = torch.empty(N, K, dtype=torch.float8_e4m3fn, device="cuda")
+    sb = torch.empty(-(-N // 128), -(-K // 128), device="cuda")
+    for i in range(0, N, 1280):  # whole blocks of rows at a time
+        qb[i:i + 1280], sb[i // 128:i // 128 + 10] = fp8.quantize_blocks(r(min(1280, N - i), K))
+    d = fp8.block_matmul(qa, sa, qb, sb, out_dtype=torch.float32)
+    cols = [0, 127, 128, 4999, 9599, 9600]
+    b = _np(qb[cols].float()) * np.repeat(_np(sb)[np.array(cols) // 128], 128, 1)[:, :K]
+    a = _np(qa.float()) * np.repeat(_np(sa), 128, 1)[:, :K]
+    _close(_np(d[:, cols]), a @ b.T, (np.abs(a) @ np.abs(b).T) * 2 * (K + K // 128 + 8) * U)
+
+
 @pytest.mark.parametrize("M", [3, 130])
 def test_block_matmul_rows_do_not_depend_on_the_batch(M):
     """Twice the same, and (within one kernel's range of M) a row's result does
@@ -410,6 +438,22 @@ def test_logprobs_masks(dtype, V):
             if T < 1 and low != -float("inf"):
                 continue  # the row of lowest values: its lse leaves fp32
             _check_logprobs(z, t, min(V, 20), T=T)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("scale", [1e-30, 1e-3, 3e4, 1e30, 3e37])
+def test_logprobs_magnitudes(dtype, scale):
+    """Logits and temperatures of any size, with masked places: what a maximum less
+    200 powers of two is rounds to the maximum, or leaves the type's range."""
+    z, t = _logits(5, 6007, dtype, 11)
+    z = (z.float() * scale / 3).to(DT[dtype])
+    z[0, ::3] = -float("inf")
+    z[1, 1::2] = torch.finfo(DT[dtype]).min
+    z[2] = z[2, 0]
+    t[0], t[1] = 1, 0
+    _check_logprobs(z, t, 7, T=float(np.float32(scale)), grads=scale < 1e20)
+    if scale == 3e4:  # differences far beyond what an exponential holds
+        _check_logprobs(z, t, 7, T=1.0)
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
