@@ -221,17 +221,11 @@ flkl_status fp8_matmul(const Fp8Call& c) {
 }
 
 // --------------------------------------------------------- log-probabilities
-template <typename T, bool TOP>
-flkl_status launch_logprobs(const LpFwdArgs& a, cudaStream_t st) {
-  // CTAs per row: a power of two up to 8 that brings two CTAs to each SM, as
-  // long as each has a tile of its own
-  int parts = 1;
-  while (parts < 8 && int64_t(a.rows) * parts * 2 <= 2 * device_sms() &&
-         a.V / (parts * 2) >= LP_NT * 16 / static_cast<int>(sizeof(T)))
-    parts *= 2;
+template <typename T, bool TOP, int NT>
+flkl_status launch_logprobs_nt(const LpFwdArgs& a, int parts, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(int64_t(a.rows) * parts));
-  cfg.blockDim = dim3(LP_NT);
+  cfg.blockDim = dim3(NT);
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
@@ -239,8 +233,21 @@ flkl_status launch_logprobs(const LpFwdArgs& a, cudaStream_t st) {
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = parts > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k_token_logprobs<T, TOP>, a) == cudaSuccess ? FLKL_OK
-                                                                             : FLKL_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k_token_logprobs<T, TOP, NT>, a) == cudaSuccess ? FLKL_OK
+                                                                                 : FLKL_ERR_CUDA;
+}
+
+template <typename T, bool TOP>
+flkl_status launch_logprobs(const LpFwdArgs& a, cudaStream_t st) {
+  // CTAs per row: a power of two up to 8 that brings two CTAs to each SM, as
+  // long as each has a tile of its own
+  int parts = 1;
+  while (parts < 8 && int64_t(a.rows) * parts * 2 <= 2 * device_sms() &&
+         a.V / (parts * 2) >= 256 * 16 / static_cast<int>(sizeof(T)))
+    parts *= 2;
+  if (parts == 1 && int64_t(a.V) * sizeof(T) <= 160 * 1024)
+    return launch_logprobs_nt<T, TOP, 128>(a, 1, st);
+  return launch_logprobs_nt<T, TOP, 256>(a, parts, st);
 }
 
 }  // namespace

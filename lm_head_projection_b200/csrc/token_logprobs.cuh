@@ -13,12 +13,13 @@
 // at -200, below which 2^t is 0 in fp32 (0 times -infinity would not be).
 //
 // The k best cost the pass next to nothing: each thread's running maximum is the
-// largest of its 1/256 of the row.  Where each of the 8 warps has k / 8 maxima
-// that reach a bound, at least k logits do, and only the threads that reach it
-// (21 on average with k up to 8, 54 with 32) hold such logits.  The few of their
-// vectors that hold any are read again (a thread leaves the maximum of every 4
-// vectors in shared memory), and what passes goes to a list there as 64-bit keys
-// (ordered value, then the lower index first), which is cut to its k best.
+// largest of its 1/NT of the row.  Where each of the W warps has k / W maxima that
+// reach a bound, at least k logits do, and only the threads that reach it
+// (of 256 threads 21 on average with k up to 8, 54 with 32) hold such logits.  The
+// few of their vectors that hold any are read again (a thread leaves the maximum
+// of every 4 vectors in shared memory), and what passes goes to a list there as
+// 64-bit keys (ordered value, then the lower index first), which is cut to its k
+// best.
 //
 // Ties: where many threads reach the bound (rows of equal logits, masks of one
 // value with less than k tokens left), the bound is raised to the k-th largest of
@@ -44,15 +45,22 @@
 
 namespace flkl {
 
-constexpr int LP_NT = 256;          // threads per CTA
 constexpr int LP_U = 4;             // 16-byte vectors per thread and tile
-constexpr int LP_CTAS = 4;          // CTAs per SM (64 registers a thread)
-constexpr int LP_TILE = LP_NT * LP_U;  // vectors per CTA and tile
 constexpr int LP_MAX_K = 32;        // alternatives at most (one per lane)
 constexpr int LP_TRIG = 64;         // appended keys above k that make a cut worth it
-constexpr int LP_CAP = LP_NT * 8 + LP_MAX_K + LP_TRIG + 32;  // keys the list holds
 constexpr int LP_MAX_REACH = 96;    // threads that reach the bound: more are ties
 constexpr int LP_SLOTS = 32;        // maxima that a thread leaves
+constexpr int LP_SM_THREADS = 1024; // threads that stand on an SM (64 registers each)
+
+// NT threads per CTA: 256, or 128 for short rows, whose tiles then waste less and
+// whose ends cost less (4000 x 10000 bf16 with 5 alternatives 65 -> 44 us, 4000 x
+// 50257 110 -> 99 us; 1024 x 151936 68 -> 71 us).
+template <int NT>
+__host__ __device__ constexpr int lp_tile() { return NT * LP_U; }  // vectors per CTA and tile
+template <int NT>
+__host__ __device__ constexpr int lp_cap() {  // keys the list holds
+  return NT * 8 + LP_MAX_K + LP_TRIG + 32;
+}
 
 struct LpFwdArgs {
   const void* logits;
@@ -217,22 +225,24 @@ __device__ __forceinline__ K warp_merge_desc(K v, K w_rev, int lane) {
   return v;
 }
 
+template <int NT>
 struct LpTopSmem {
-  unsigned long long buf[LP_CAP];
-  unsigned long long part[LP_NT / 32][32];
-  uint16_t slot[LP_SLOTS][LP_NT];  // the maxima's upper 16 bits (a bf16 number, cut)
-  uint16_t item[LP_MAX_REACH * LP_SLOTS];  // slot * LP_NT + thread
+  unsigned long long buf[lp_cap<NT>()];
+  unsigned long long part[NT / 32][32];
+  uint16_t slot[LP_SLOTS][NT];  // the maxima's upper 16 bits (a bf16 number, cut)
+  uint16_t item[LP_MAX_REACH * LP_SLOTS];  // slot * NT + thread
   int cnt, items;
   uint32_t bound;
 };
 
 // Cuts the list to its k best, buf[0..32) descending (0 past them).  Called by
 // all threads after a barrier that makes the keys visible; ends with one.
-__device__ __forceinline__ void lp_cut(LpTopSmem& s, int k) {
+template <int NT>
+__device__ __forceinline__ void lp_cut(LpTopSmem<NT>& s, int k) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = s.cnt;
   __syncthreads();  // everyone has read the count
-  if (c <= LP_NT) {  // a key's place is the number of larger ones
+  if (c <= NT) {  // a key's place is the number of larger ones
     unsigned long long key = 0;
     int place = 0;
     if (threadIdx.x < c) {
@@ -248,12 +258,12 @@ __device__ __forceinline__ void lp_cut(LpTopSmem& s, int k) {
     return;
   }
   unsigned long long best = 0;
-  for (int b = warp * 32; b < c; b += LP_NT) {
+  for (int b = warp * 32; b < c; b += NT) {
     unsigned long long v = b + lane < c ? s.buf[b + lane] : 0ull;
     v = warp_sort_desc(v, lane);
     best = warp_merge_desc(best, __shfl_sync(0xffffffffu, v, 31 - lane), lane);
   }
-  const int lists = min(LP_NT / 32, (c + 31) / 32);
+  const int lists = min(NT / 32, (c + 31) / 32);
   if (lists > 1) {
     s.part[warp][lane] = best;
     __syncthreads();
@@ -267,30 +277,30 @@ __device__ __forceinline__ void lp_cut(LpTopSmem& s, int k) {
 
 // One CTA's share of a row: 16-byte vectors [v0, v1) from zv (logit head + E v
 // on) and `extra` single logits before the first and after the last vector;
-// thread t has vectors v0 + t, v0 + t + 256, ... and single t.
-template <typename T>
+// thread t has vectors v0 + t, v0 + t + NT, ... and single t.
+template <typename T, int NT>
 struct LpPart {
   using VT = LpVec<T>;
   const T* z;
   const uint4* zv;
   int v0, v1, head, tail0, own_head, extra;
-  // tiles (of LP_TILE vectors) per slot: 2^this
+  // tiles (of lp_tile<NT>() vectors) per slot: 2^this
   __device__ int slot_shift() const {
     int sh = 0;
-    while ((v1 - v0 - 1) / LP_TILE >> sh >= LP_SLOTS) ++sh;
+    while ((v1 - v0 - 1) / lp_tile<NT>() >> sh >= LP_SLOTS) ++sh;
     return sh;
   }
   __device__ int extra_index(int i) const { return i < own_head ? i : tail0 + i - own_head; }
 
-  __device__ void append(LpTopSmem& s, float f, int idx) const {
+  __device__ void append(LpTopSmem<NT>& s, float f, int idx) const {
     const int p = atomicAdd(&s.cnt, 1);
-    if (p < LP_CAP) s.buf[p] = lp_key(f, static_cast<uint32_t>(idx));
+    if (p < lp_cap<NT>()) s.buf[p] = lp_key(f, static_cast<uint32_t>(idx));
   }
   // Logits of vector i from order value lo on (with `only`: of just that value).
-  __device__ void append_vec(LpTopSmem& s, int i, uint32_t lo, bool only) const {
+  __device__ void append_vec(LpTopSmem<NT>& s, int i, uint32_t lo, bool only) const {
     append_raw(s, ld_nc_v4(zv + i), i, lo, only);
   }
-  __device__ void append_raw(LpTopSmem& s, const uint4& raw, int i, uint32_t lo,
+  __device__ void append_raw(LpTopSmem<NT>& s, const uint4& raw, int i, uint32_t lo,
                              bool only) const {
     if (lp_ord(VT::max(raw)) < lo) return;
     float f[VT::E];
@@ -301,7 +311,7 @@ struct LpPart {
       if (only ? o == lo : o >= lo) append(s, f[j], head + i * VT::E + j);
     }
   }
-  __device__ void append_one(LpTopSmem& s, int i, uint32_t lo, bool only) const {
+  __device__ void append_one(LpTopSmem<NT>& s, int i, uint32_t lo, bool only) const {
     const int idx = extra_index(i);
     const float f = VT::one(z + idx);
     const uint32_t o = lp_ord(f);
@@ -310,9 +320,9 @@ struct LpPart {
 
   // All logits from order value lo on that threads with own >= lo hold, into
   // the empty list; returns their number (which may exceed the list).
-  __device__ int collect(LpTopSmem& s, uint32_t own, uint32_t lo) const {
+  __device__ int collect(LpTopSmem<NT>& s, uint32_t own, uint32_t lo) const {
     const int tid = threadIdx.x;
-    const int sh = slot_shift(), tiles = (v1 - v0 + LP_TILE - 1) / LP_TILE;
+    const int sh = slot_shift(), tiles = (v1 - v0 + lp_tile<NT>() - 1) / lp_tile<NT>();
     // (cutting keeps the order, so that no slot that holds such a logit is missed)
     const uint32_t lo16 =
         lo == 0 ? 0u : lp_ord(__uint_as_float(__float_as_uint(lp_unord(lo)) & 0xFFFF0000u));
@@ -324,16 +334,16 @@ struct LpPart {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if ((q0 + i) << sh < tiles && lp_ord(__uint_as_float(m[i])) >= lo16)
-            s.item[atomicAdd(&s.items, 1)] = static_cast<uint16_t>((q0 + i) * LP_NT + tid);
+            s.item[atomicAdd(&s.items, 1)] = static_cast<uint16_t>((q0 + i) * NT + tid);
       }
       if (tid < extra) append_one(s, tid, lo, false);
     }
     __syncthreads();
     // the vectors of those slots, one per thread whoever's they were
     const int per = LP_U << sh, n = s.items * per;
-    for (int w = tid; w < n; w += LP_NT) {
+    for (int w = tid; w < n; w += NT) {
       const int it = s.item[w / per], u = w % per;
-      const int i = v0 + (it / LP_NT << sh) * LP_TILE + u * LP_NT + it % LP_NT;
+      const int i = v0 + (it / NT << sh) * lp_tile<NT>() + u * NT + it % NT;
       if (i < v1) append_vec(s, i, lo, false);
     }
     __syncthreads();
@@ -341,15 +351,15 @@ struct LpPart {
   }
   // The k best (or all) from order value lo on, in rounds over the whole part in
   // index order: what ties with the k-th of a cut list comes later and loses.
-  __device__ void rounds(LpTopSmem& s, uint32_t lo, int k) const {
+  __device__ void rounds(LpTopSmem<NT>& s, uint32_t lo, int k) const {
     const int tid = threadIdx.x;
     __syncthreads();  // everyone has read the count
     if (tid == 0) s.cnt = 0;
     __syncthreads();
     if (tid < own_head) append_one(s, tid, lo, false);
-    for (int b = v0; b < v1 || b == v0; b += LP_NT) {
+    for (int b = v0; b < v1 || b == v0; b += NT) {
       if (b + tid < v1) append_vec(s, b + tid, lo, false);
-      if (b + LP_NT >= v1 && tid >= own_head && tid < extra) append_one(s, tid, lo, false);
+      if (b + NT >= v1 && tid >= own_head && tid < extra) append_one(s, tid, lo, false);
       __syncthreads();
       const int n = s.cnt;
       __syncthreads();
@@ -364,12 +374,12 @@ struct LpPart {
     lp_cut(s, k);
   }
   // Logits of order value `eq`, in index order, until the list holds k.
-  __device__ void equals(LpTopSmem& s, uint32_t eq, int k) const {
+  __device__ void equals(LpTopSmem<NT>& s, uint32_t eq, int k) const {
     const int tid = threadIdx.x;
     if (tid < own_head) append_one(s, tid, eq, true);
-    for (int b = v0; b < v1 || b == v0; b += LP_NT) {
+    for (int b = v0; b < v1 || b == v0; b += NT) {
       if (b + tid < v1) append_vec(s, b + tid, eq, true);
-      if (b + LP_NT >= v1 && tid >= own_head && tid < extra) append_one(s, tid, eq, true);
+      if (b + NT >= v1 && tid >= own_head && tid < extra) append_one(s, tid, eq, true);
       __syncthreads();
       const int n = s.cnt;
       __syncthreads();
@@ -378,12 +388,12 @@ struct LpPart {
   }
   // buf[0..32): the part's k best, descending.  `own` is the order value of the
   // thread's largest logit (0: it has none).
-  __device__ void top(LpTopSmem& s, uint32_t own, int k) const {
+  __device__ void top(LpTopSmem<NT>& s, uint32_t own, int k) const {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // a bound that k maxima reach: each warp's ((k + 7) / 8)-th largest, the
-    // smallest of the 8
+    // a bound that k maxima reach: each warp's (k / warps)-th largest, rounded up,
+    // the smallest of them
     uint32_t rest = own, rth = 0;
-    for (int i = (k + 7) / 8; i > 0; --i) {
+    for (int i = (k + NT / 32 - 1) / (NT / 32); i > 0; --i) {
       rth = __reduce_max_sync(0xffffffffu, rest);
       if (lane == __ffs(__ballot_sync(0xffffffffu, rest == rth)) - 1) rest = 0;
     }
@@ -393,17 +403,17 @@ struct LpPart {
     __syncthreads();
     uint32_t lo = part[0][0];
 #pragma unroll
-    for (int w = 1; w < LP_NT / 32; ++w) lo = min(lo, part[0][w]);
+    for (int w = 1; w < NT / 32; ++w) lo = min(lo, part[0][w]);
     // (a bound of 0: a thread without logits, and so at most one slot a thread)
     int reach = __syncthreads_count(own >= lo && own > 0);
     if (reach > LP_MAX_REACH && lo != 0) {
-      // the k-th largest of all maxima: each warp's in order, then the 8 lists
+      // the k-th largest of all maxima: each warp's in order, then the lists
       // merged in pairs
       uint32_t best = warp_sort_desc(own, lane);
       part[warp][lane] = best;
       __syncthreads();
 #pragma unroll
-      for (int n = LP_NT / 64; n >= 1; n >>= 1) {
+      for (int n = NT / 64; n >= 1; n >>= 1) {
         if (warp < n) {
           best = warp_merge_desc(best, part[warp + n][31 - lane], lane);
           part[warp][lane] = best;
@@ -416,12 +426,12 @@ struct LpPart {
     }
     if (reach <= LP_MAX_REACH || lo == 0) {
       const int n = collect(s, own, lo);
-      if (n <= LP_CAP) lp_cut(s, k);
+      if (n <= lp_cap<NT>()) lp_cut(s, k);
       else rounds(s, lo, k);
       return;
     }
     const int n = lo == 0xFFFFFFFFu ? 0 : collect(s, own, lo + 1);
-    if (n > LP_CAP) {
+    if (n > lp_cap<NT>()) {
       rounds(s, lo + 1, k);
       return;
     }
@@ -431,17 +441,18 @@ struct LpPart {
   }
 };
 
+template <int NT>
 struct LpShared {
-  float3 red[LP_NT / 32];
+  float3 red[NT / 32];
   float3 sums;  // the CTA's, read by the cluster's first
 };
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(LP_NT, LP_CTAS) k_token_logprobs(const LpFwdArgs a) {
+template <typename T, bool TOP, int NT>
+__global__ void __launch_bounds__(NT, LP_SM_THREADS / NT) k_token_logprobs(const LpFwdArgs a) {
   using VT = LpVec<T>;
   constexpr int E = VT::E;
-  __shared__ LpShared sh;
-  __shared__ typename std::conditional<TOP, LpTopSmem, int>::type top_mem;
+  __shared__ LpShared<NT> sh;
+  __shared__ typename std::conditional<TOP, LpTopSmem<NT>, int>::type top_mem;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t parts;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(parts));
@@ -463,7 +474,7 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS) k_token_logprobs(const LpFwdAr
     }
     return;
   }
-  LpPart<T> p;
+  LpPart<T, NT> p;
   p.z = static_cast<const T*>(a.logits) + static_cast<long long>(row) * a.ld;
   const float zy = y >= 0 && y < a.V ? VT::one(p.z + y) : 0.f;
   const float c = 1.4426950408889634f / a.temperature;
@@ -504,25 +515,25 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS) k_token_logprobs(const LpFwdAr
   auto fetch = [&](int b) {
 #pragma unroll
     for (int u = 0; u < LP_U; ++u) {
-      const int i = b + u * LP_NT + tid;
+      const int i = b + u * NT + tid;
       next[u] = i < p.v1 ? ld_nc_v4(p.zv + i) : VT::empty();
     }
   };
   fetch(p.v0);
-  const uint4* ahead = p.zv + p.v0 + LP_TILE + tid;  // this thread's first vector there
+  const uint4* ahead = p.zv + p.v0 + lp_tile<NT>() + tid;  // this thread's first vector there
   const int shift = TOP ? p.slot_shift() : 0;
   int tile = 0;
   float slot_max = -INFINITY;
-  for (int b = p.v0; b < p.v1; b += LP_TILE) {
+  for (int b = p.v0; b < p.v1; b += lp_tile<NT>()) {
     uint4 raw[LP_U];
 #pragma unroll
     for (int u = 0; u < LP_U; ++u) raw[u] = next[u];
-    if (b + 2 * LP_TILE <= p.v1) {  // (whole tiles need no look at their end)
+    if (b + 2 * lp_tile<NT>() <= p.v1) {  // (whole tiles need no look at their end)
 #pragma unroll
-      for (int u = 0; u < LP_U; ++u) next[u] = ld_nc_v4(ahead + u * LP_NT);
-      ahead += LP_TILE;
+      for (int u = 0; u < LP_U; ++u) next[u] = ld_nc_v4(ahead + u * NT);
+      ahead += lp_tile<NT>();
     } else {
-      fetch(b + LP_TILE);
+      fetch(b + lp_tile<NT>());
     }
     const float tm = VT::max4(raw);
     if constexpr (TOP) {
@@ -556,7 +567,7 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS) k_token_logprobs(const LpFwdAr
     } else if (sum.m > -INFINITY) {
 #pragma unroll
       for (int u = 0; u < LP_U; ++u) {
-        if (b + u * LP_NT + warp * 32 >= p.v1) break;
+        if (b + u * NT + warp * 32 >= p.v1) break;
         float f[E];
         VT::unpack(raw[u], f);
 #pragma unroll
@@ -583,7 +594,7 @@ __global__ void __launch_bounds__(LP_NT, LP_CTAS) k_token_logprobs(const LpFwdAr
   if (warp == 0) {
     sum.init();
 #pragma unroll
-    for (int w = 0; w < LP_NT / 32; ++w) sum.merge(sh.red[w].x, sh.red[w].y, sh.red[w].z, c);
+    for (int w = 0; w < NT / 32; ++w) sum.merge(sh.red[w].x, sh.red[w].y, sh.red[w].z, c);
     if constexpr (TOP) best = top_mem.buf[lane];
   }
   if (parts > 1) {
