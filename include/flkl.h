@@ -408,6 +408,10 @@ FLKL_API flkl_status flkl_layer_norm_backward(const void* dY, const void* X, con
  *   h = round(X + residual),  y = W h / sqrt(mean(h^2) + eps)
  *   scale[r][j] = max |y[r][128 j ..]| / 448,  code = e4m3(y / scale)
  *
+ * Codes are the nearest ones, ties to even: of bf16 inputs exactly those of
+ * 448 W h / max |W h|, in which the root cancels; of fp32 inputs up to a few
+ * roundings of fp32 beside a tie.
+ *
  *  X, residual  device [rows, H], W [H], `dtype`; residual may be NULL, then
  *               h = X and Hs must be NULL.
  *  rows, H, eps as below (flkl_rms_norm_backward), rows below 2^31.
@@ -438,8 +442,9 @@ FLKL_API flkl_status flkl_add_rms_norm_backward(const void* dY, const void* dH, 
 /* e4m3 codes with fp32 scales of a dense [rows, cols] matrix: one scale per
  * row and 128 columns (block_rows = 1, activations) or per 128 x 128 block
  * (block_rows = 128, weights): scale = max |src| over the block / 448, code =
- * e4m3(src / scale), rounded to nearest even; the last block of a row or
- * column may be short.
+ * e4m3(448 src / max |src|), rounded to nearest even (bf16: exactly so; fp32:
+ * within 2^-21 of a tie either way); the last block of a row or column may be
+ * short.
  *  src    device [rows, cols], `dtype`; cols a multiple of 16.
  *  q      device [rows, cols] bytes (overwritten).
  *  scale  device fp32 [ceil(rows / block_rows), ceil(cols / 128)].

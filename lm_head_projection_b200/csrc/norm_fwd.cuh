@@ -6,7 +6,10 @@
 //
 // y is formed from the rounded h, the value that the residual stream keeps, so
 // that the backward pass, which reads h, differentiates what was computed.
-// The 8-bit output is rounded once, from the fp32 y.
+// The 8-bit output is rounded once: r falls out of y / max |y|, so that codes are
+// formed from p = 2^e h w, with 2^e the power of two in r.  p has y's size and,
+// where the row is bf16, is exact, so that codes are the nearest ones and exact
+// ties go to even (fp8.cuh); the scale is max |p| r / 2^e / 448.
 //
 // HBM-bound (bf16 in, e4m3 out: 7 bytes per element and nothing to reuse), so a
 // row is read once into registers, 8 columns per thread and vector, and every
@@ -85,6 +88,18 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 2048 / NT : 1)
     for (int i = 1; i < NW; ++i) ss += red[i];
   }
   const float rinv = rsqrtf(ss / static_cast<float>(H) + a.eps);
+  // 8 bits: 2^e, and what is left of rinv (infinity and NaN are passed on whole)
+  float factor = rinv, rest = 1.f;
+  if constexpr (QUANT) {
+    if (rinv < INFINITY) {
+      factor = __uint_as_float(__float_as_uint(rinv) & 0x7F800000u);
+      rest = rinv * __uint_as_float(0x7F000000u - __float_as_uint(factor));
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[v][i] *= factor;
   const T* W = static_cast<const T*>(a.W);
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
@@ -93,16 +108,16 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 2048 / NT : 1)
       float w[8];
       Vec8<T>::load(W + c, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) h[v][i] = h[v][i] * rinv * w[i];
+      for (int i = 0; i < 8; ++i) h[v][i] *= w[i];
     }
     if constexpr (QUANT) {
       // columns [128 j, 128 j + 128) are one half warp's (G is a multiple of 32)
-      const float m = half_warp_max(amax8(h[v]));
+      const float m = half_warp_max(amax8(h[v])), ymax = m * rest;
       if (c < H) {
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.Y) + off + c) =
-            e4m3_pack8(h[v], e4m3_inv_scale(m));
+            e4m3_pack8(h[v], e4m3_tiny(ymax) ? 1.f : e4m3_inverse(m));
         if ((lane & 15) == 0)
-          a.scale[static_cast<size_t>(row) * ((H + 127) / 128) + c / 128] = e4m3_scale(m);
+          a.scale[static_cast<size_t>(row) * ((H + 127) / 128) + c / 128] = e4m3_scale(ymax);
       }
     } else {
       if (c < H) Vec8<T>::store(static_cast<T*>(a.Y) + off + c, h[v]);

@@ -24,6 +24,26 @@ def e4m3_round(x):
     return np.sign(x) * np.minimum(np.rint(a / step) * step, E4M3_MAX)
 
 
+def e4m3_quotients(v, m):
+    """448 v / m to the nearest e4m3 number, ties to even, in whole numbers: v and m
+    (m > 0, |v| <= m) have at most 24 significant bits."""
+    v, m = np.broadcast_arrays(np.asarray(v, np.float64), np.asarray(m, np.float64))
+    fv, ev = np.frexp(np.abs(v))
+    fm, em = np.frexp(m)
+    num = 448 * np.ldexp(fv, 24).astype(np.int64)  # the quotient is num / den * 2^(ev - em)
+    den = np.ldexp(fm, 24).astype(np.int64)
+    sh = ev - em
+    # leading power of two: 2^e <= quotient
+    e = np.floor(np.log2(np.where(num > 0, num / den, 1.0))).astype(np.int64) + sh
+    step = np.maximum(e, -6) - 3
+    up = np.clip(sh - step, -60, 60)
+    num = np.where(up > 0, num << np.clip(up, 0, 25), num)  # (num / den 2^up < 16)
+    den = np.where(up < 0, den << np.clip(-up, 0, 38), den)
+    n, r = num // den, num % den
+    n = n + ((2 * r > den) | ((2 * r == den) & (n % 2 == 1)))
+    return np.sign(v) * np.ldexp(n.astype(np.float64), step.astype(np.int32))
+
+
 def _blocks(k):
     return [(i, min(i + 128, k)) for i in range(0, k, 128)]
 

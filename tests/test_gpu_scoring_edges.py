@@ -1,0 +1,113 @@
+"""Edges of the scoring path on the GPU, beside tests/test_gpu_scoring.py: codes at
+exact ties."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import scoring_oracle as o
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+HALF = {"fp32": 2.0 ** -24, "bf16": 2.0 ** -8}
+DT = {"fp32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _np(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def _same_codes(codes, v, block_rows=1):
+    """Codes are 448 v / max |v| rounded exactly (v in fp64, exact)."""
+    m = o.block_scales(v, block_rows) * 448  # (only for its blocks' shape)
+    for i in range(m.shape[0]):
+        for j in range(m.shape[1]):
+            r, c = slice(i * block_rows, (i + 1) * block_rows), slice(128 * j, 128 * j + 128)
+            top = np.abs(v[r, c]).max()
+            want = o.e4m3_quotients(v[r, c], top)
+            assert np.array_equal(codes[r, c], want), (i, j)
+
+
+# --------------------------------------------------------- codes at exact ties
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("block", [1, 128])
+def test_quantizer_codes_of_every_pair_of_short_values(dtype, block):
+    """Every significand of bf16 against every largest value's, over all the
+    exponents that have a code: the nearest code, ties to even."""
+    from lm_head_projection_b200 import fp8
+
+    sig = np.arange(128, 256) / 128.0
+    per = np.concatenate([sig * 2.0 ** -e for e in range(0, 20)])  # 2560 values
+    rows = []
+    for m in sig:
+        v = np.where(per <= m, per, 0.0)
+        blocks = np.zeros((21, 128))
+        blocks[:, 0] = m
+        blocks[:, 1:].reshape(-1)[:] = 0
+        flat = np.zeros(21 * 127)
+        flat[:v.size] = v
+        blocks[:, 1:] = flat.reshape(21, 127)
+        rows.append(blocks)
+    x = np.concatenate(rows)  # [2688, 128]: a row is one block
+    x[1::2] *= -1.0
+    x[::3] *= 2.0 ** 40
+    x[1::3] *= 2.0 ** -40
+    x[5, 0] = x[5, 0] * 2.0 ** 126  # the largest of the type's range
+    if block == 128:
+        # a row of 128 x 128 blocks: each has one of the rows above, spread out
+        y = np.zeros((128, 128 * len(x)))
+        for i, row in enumerate(x):
+            y[np.arange(128), 128 * i + (np.arange(128) * 37 + i) % 128] = row
+        x = y
+    t = torch.from_numpy(x).to(DT[dtype])
+    assert np.array_equal(_np(t), x)
+    q, _ = (fp8.quantize_rows if block == 1 else fp8.quantize_blocks)(t.cuda())
+    _same_codes(_np(q.float()), x, block)
+
+
+@pytest.mark.parametrize("rows,H", [(300, 136), (64, 1024), (33, 2048), (40, 4096), (30, 8192)])
+@pytest.mark.parametrize("residual", [True, False])
+def test_norm_codes_are_the_nearest(rows, H, residual):
+    """bf16 rows: the codes of W h over the block's largest, in exact arithmetic;
+    of random rows about one in two thousand lies at a tie."""
+    from lm_head_projection_b200 import norm
+
+    g = torch.Generator().manual_seed(rows + H)
+    x, r = (torch.randn(rows, H, generator=g).bfloat16() for _ in range(2))
+    w = (1 + 0.1 * torch.randn(H, generator=g)).bfloat16()
+    x[0] = (x[0] * 16).round() / 16  # short values: many ties
+    x[1] = x[1] * 2.0 ** 50
+    x[2] = x[2] * 2.0 ** -30
+    r[0] = 0
+    w[: H // 2] = 1.0
+    got = norm.add_rms_norm(x.cuda(), w.cuda(), r.cuda() if residual else None, quantize=True)
+    p = _np(got["H"]) * _np(w)
+    s = _np(got["scale"])
+    # (where a block of y is below 2^-100 its codes are 0: none here)
+    assert (s > 2.0 ** -90).all()
+    _same_codes(_np(got["Y"].float()), p)
+    y, _ = o.add_rms_norm(_np(got["H"]), None, _np(w), 1e-6, "bf16")
+    want = o.block_scales(y, 1)
+    # the sum of squares 37 u, halved by the root, its reciprocal and three products
+    assert (np.abs(s - want) <= want * 32 * U).all()
+
+
+def test_norm_codes_of_extreme_rows():
+    """Rows whose sum of squares leaves fp32, zeros, tiny rows: as before."""
+    from lm_head_projection_b200 import norm
+
+    x = torch.randn(6, 256).cuda()
+    x[0] = 1e-45
+    x[1] = 1e-36
+    x[2] *= 1e25          # squares overflow: r = 0
+    x[3] = 0
+    x[4, 7] = float("inf")
+    x[5, 200] = float("nan")
+    w = torch.ones(256).cuda()
+    q = norm.add_rms_norm(x, w, quantize=True)
+    c, s = q["Y"].float(), q["scale"]
+    assert (c[:4] == 0).all() and (s[:4] == 1).all()
+    assert torch.isnan(c[4, 7]) and (c[4, :7] == 0).all() and (c[4, 8:] == 0).all()
+    assert torch.isnan(c[5]).all()

@@ -1,0 +1,35 @@
+"""The scoring path's edges that need no GPU: the oracle's exact e4m3 quotients
+and what the Python layer refuses."""
+
+from __future__ import annotations
+
+from fractions import Fraction
+
+import numpy as np
+
+from oracle import scoring_oracle as o
+
+
+def _nearest_e4m3(q: Fraction) -> float:
+    """The nearest e4m3 number to a fraction in [-448, 448], by trying them all."""
+    every = [Fraction(k, 512) for k in range(8)]
+    every += [Fraction(8 + k) * Fraction(2) ** (e - 3) for e in range(-6, 9) for k in range(8)]
+    every = [f for f in every if f <= 448]
+    a = abs(q)
+    d = [abs(f - a) for f in every]
+    i = min(range(len(every)), key=lambda j: (d[j], j % 2))  # (the j-th has the code j)
+    return float(every[i]) * (-1 if q < 0 else 1)
+
+
+def test_exact_quotients_against_fractions():
+    rs = np.random.RandomState(0)
+    m = rs.randint(128, 256, 3000) * 2.0 ** rs.randint(-20, 20, 3000)
+    v = np.minimum(rs.randint(128, 256, 3000) * 2.0 ** rs.randint(-16, 1, 3000) / 256, 1)
+    v = np.where(v * m <= m, np.round(v * 256) / 256 * 2.0 ** rs.randint(-16, 1, 3000), 1.0)
+    v = v * 2.0 ** np.floor(np.log2(m)) * rs.choice([-1, 1], 3000)
+    v[:200] = m[:200] * rs.choice([1.0, 0.5, 15 / 16, 31 / 32, 2.0 ** -18, 0.0], 200)
+    got = o.e4m3_quotients(v, m)
+    for x, d, g in zip(v, m, got):
+        assert g == _nearest_e4m3(448 * Fraction(float(x)) / Fraction(float(d))), (x, d)
+    # ties go to even: 17 / 448 of the largest lies between codes 16 and 18
+    assert o.e4m3_quotients(17.0, 448.0) == 16 and o.e4m3_quotients(-19.0, 448.0) == -20
