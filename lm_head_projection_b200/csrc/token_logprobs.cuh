@@ -493,7 +493,9 @@ __global__ void __launch_bounds__(NT, LP_SM_THREADS / NT) k_token_logprobs(const
   sum.init();
   // bf16: what lies 200 powers of two below the maximum has 2^t = 0, so logits
   // are first raised to there, two at a time, where that is a finite number
-  // (`near`): then no t is -infinity and needs a look of its own.
+  // (`near`): then no t is -infinity and needs a look of its own.  The bf16 number
+  // is up to |l| / 128 lower, which a small temperature may scale beyond fp32
+  // (|m| / T above about 1e40): such rows take the other way, too.
   const float reach = 200.f / c;
   bool near = false;
   uint32_t lo2 = 0;
@@ -501,9 +503,10 @@ __global__ void __launch_bounds__(NT, LP_SM_THREADS / NT) k_token_logprobs(const
     sum.raise(m, c);
     if constexpr (E == 8) {
       const float l = m - reach;
-      near = l > -3.3e38f && m < 3e38f;
       // a bf16 number below l, and so below m even where m - reach rounds to m
-      lo2 = __bfloat16_as_ushort(__float2bfloat16_rd(l - fabsf(l) * 0x1p-8f)) * 0x10001u;
+      const __nv_bfloat16 lo = __float2bfloat16_rd(l - fabsf(l) * 0x1p-8f);
+      near = l > -3.3e38f && m < 3e38f && (m - __bfloat162float(lo)) * c < 1e30f;
+      lo2 = __bfloat16_as_ushort(lo) * 0x10001u;
     }
   };
   if (tid < p.extra) {  // at most 2 (E - 1) single logits

@@ -1,5 +1,5 @@
 """Edges of the scoring path on the GPU, beside tests/test_gpu_scoring.py: codes at
-exact ties."""
+exact ties, log-probabilities where logits over temperature leave fp32."""
 
 from __future__ import annotations
 
@@ -8,15 +8,9 @@ import pytest
 import torch
 
 from oracle import scoring_oracle as o
+from tests.test_gpu_scoring import DT, HALF, U, _close, _np, tol
 
 pytestmark = pytest.mark.gpu
-U = 2.0 ** -24
-HALF = {"fp32": 2.0 ** -24, "bf16": 2.0 ** -8}
-DT = {"fp32": torch.float32, "bf16": torch.bfloat16}
-
-
-def _np(t):
-    return None if t is None else t.detach().double().cpu().numpy()
 
 
 def _same_codes(codes, v, block_rows=1):
@@ -111,3 +105,48 @@ def test_norm_codes_of_extreme_rows():
     assert (c[:4] == 0).all() and (s[:4] == 1).all()
     assert torch.isnan(c[4, 7]) and (c[4, :7] == 0).all() and (c[4, 8:] == 0).all()
     assert torch.isnan(c[5]).all()
+
+
+# ------------------------------------- log-probabilities beyond fp32's |m| / T
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("V", [7, 1000, 8192, 5003])
+@pytest.mark.parametrize("m,T", [(-1e38, 1e-3), (-1e36, 1e-5), (-1e37, 1e-4), (1e38, 1e-3),
+                                 (1e5, 1e-36), (-3e38, 0.5)])
+def test_logprobs_of_rows_far_beyond_the_temperature(dtype, V, m, T):
+    """Rows of one value, as a mask of a large finite number leaves them, whole,
+    partly masked with -infinity or with one token left: the entropy is ln of the
+    number of tokens that share the maximum and no gradient is NaN."""
+    from lm_head_projection_b200 import logprobs
+
+    T = float(np.float32(T))
+    z = torch.full((5, V), m)
+    z[1, 3:] = -float("inf")
+    z[2, 1::2] = torch.finfo(DT[dtype]).min
+    z[3, V // 2] = m * (0.9 if m < 0 else 1.1)
+    z[4, ::3] = m * (1.1 if m < 0 else 0.9)
+    z = z.to(DT[dtype]).cuda()
+    t = torch.tensor([0, 1, 2, V // 2, 1]).cuda()
+    k = min(V, 6)
+    got = logprobs.token_logprobs_forward(z, t, temperature=T, top_k=k)
+    zn, tn = _np(z), t.cpu().numpy()
+    want = o.token_logprobs(zn, tn, -100, T, k)
+    big = np.finfo(np.float32).max
+    for n in ("logp", "top_logp"):  # (what leaves fp32 is infinite there)
+        w = np.where(np.abs(want[n]) > big, np.copysign(np.inf, want[n]), want[n])
+        fin = np.where(np.isfinite(w), w, 0)
+        _close(_np(got[n]), w, np.abs(fin) * 8 * U + 2 * tol(V), n)
+    assert np.array_equal(got["top_ids"].cpu().numpy(), want["top_ids"])
+    ent = want["entropy"]
+    _close(_np(got["entropy"]), ent, (3 + 2 * ent + 2 * np.log(V + 1)) * tol(V), "entropy")
+    rs = np.random.RandomState(V)
+    gl, ge = (rs.normal(size=5).astype(np.float32) for _ in range(2))
+    gt = rs.normal(size=(5, k)).astype(np.float32)
+    c = lambda a: None if a is None else torch.from_numpy(a).cuda()
+    for use in ((gl, ge, gt), (gl, None, None), (None, ge, None)):
+        dz = logprobs.token_logprobs_backward(z, t, got, c(use[0]), c(use[1]), c(use[2]),
+                                              temperature=T)
+        wz, mag = o.token_logprobs_backward(zn, tn, want, *use, -100, T)
+        # as in test_gpu_scoring.py; what 1 / T makes smaller than fp32's normal
+        # numbers may be cut
+        _close(_np(dz), wz, np.abs(wz) * HALF[dtype] + mag * (4 * tol(V) + 1200 * U)
+               + 2.0 ** -126, "dz")
