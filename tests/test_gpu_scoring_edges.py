@@ -111,7 +111,10 @@ def test_norm_codes_of_extreme_rows():
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("V", [7, 1000, 8192, 5003])
 @pytest.mark.parametrize("m,T", [(-1e38, 1e-3), (-1e36, 1e-5), (-1e37, 1e-4), (1e38, 1e-3),
-                                 (1e5, 1e-36), (-3e38, 0.5)])
+                                 (1e5, 1e-36), (-3e38, 0.5),
+                                 # differences of logits beyond fp32 that count
+                                 (2.9e38, 1.5e36), (-2e38, 2.4e36), (3e38, 3e38), (1e30, 3e38),
+                                 (3e38, 4.0)])
 def test_logprobs_of_rows_far_beyond_the_temperature(dtype, V, m, T):
     """Rows of one value, as a mask of a large finite number leaves them, whole,
     partly masked with -infinity or with one token left: the entropy is ln of the
