@@ -29,7 +29,8 @@ __all__ = [
     "FusedLinearJSDLoss", "flkl_scale_cast", "flkl_clock_trace", "flkl_gemm_ctas", "flkl_vocab_chunks",
     "flkl_forward_backward_dp_events", "flkl_ce_forward_backward_dp_events",
     "flkl_add_rms_norm_forward", "flkl_add_rms_norm_backward", "flkl_fp8_quantize",
-    "flkl_fp8_block_matmul", "flkl_fp8_device_status", "flkl_token_logprobs_forward", "flkl_token_logprobs_backward",
+    "flkl_fp8_block_matmul", "flkl_fp8_device_status", "flkl_fp8_wait_selftest",
+    "flkl_token_logprobs_forward", "flkl_token_logprobs_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -163,6 +164,8 @@ def _lib():
         lib.flkl_fp8_quantize.argtypes = [P, L, L, I, I, P, P, P]
         lib.flkl_fp8_block_matmul.restype = I
         lib.flkl_fp8_block_matmul.argtypes = [P, P, P, P, P, L, L, L, I, P, P]
+        lib.flkl_fp8_wait_selftest.restype = I
+        lib.flkl_fp8_wait_selftest.argtypes = [P, P, P, P, L, L, L, P, I, c.c_uint, c.c_uint, P]
         lib.flkl_fp8_device_status.restype = I
         lib.flkl_fp8_device_status.argtypes = [P]
         lib.flkl_token_logprobs_forward.restype = I
@@ -329,6 +332,14 @@ def flkl_fp8_block_matmul(A, a_scale, B, b_scale, bias, M, N, K, out_dtype, D, s
 def flkl_fp8_device_status(stream=None) -> int:
     """Synchronise ``stream``; status of the product's kernels since the last call."""
     return _lib().flkl_fp8_device_status(stream)
+
+
+def flkl_fp8_wait_selftest(A, a_scale, B, b_scale, M, N, K, D, role, blocks, limit_ms,
+                           stream=None) -> int:
+    """The product with a role of its kernel that stops, so that its bounded waits
+    run out (raw pointers); returns the status of the launch."""
+    return _lib().flkl_fp8_wait_selftest(A, a_scale, B, b_scale, M, N, K, D, role, blocks,
+                                         limit_ms, stream)
 
 
 def flkl_token_logprobs_forward(logits, row_stride, target, ignore_index, rows, V, dtype,

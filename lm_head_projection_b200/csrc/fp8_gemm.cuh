@@ -33,8 +33,9 @@
 // The small kernel: 1 x 128256 x 4096 92 us (525 MB, 5.7 TB/s; 1002 tiles on 148
 // SMs are 6.8 waves, the last one short); 40 x 4096 x 4096 about 6 us on the device.
 //
-// Every wait is bounded; on a timeout the CTA stops computing, lets its copies
-// and MMAs land, frees TMEM and returns, and the status word says so.
+// Every wait is bounded; on a timeout the CTA stops computing, waits (bounded
+// again) until the loads that it has issued have landed and its MMAs are done,
+// frees TMEM and returns, and the status word says so.
 #pragma once
 
 #include "ptx.cuh"
@@ -54,7 +55,12 @@ struct Fp8Gemm {
   int vec;               // k_fp8_pair: D's rows start on 16-byte boundaries
   int stages;            // k_fp8_skinny: ring depth
   unsigned long long wait_limit_ns;
+  int hold;              // Fp8Hold: a role that stops, so that the others' waits run out
+  uint32_t hold_at;      // after this many blocks
 };
+// (kernels with HOLD, which flkl_fp8_wait_selftest launches; in the others not even
+// looked at: the comparison per block cost 1 %)
+enum Fp8Hold { FP8_HOLD_NONE = 0, FP8_HOLD_MMA = 1, FP8_HOLD_LOAD = 2, FP8_HOLD_LOAD_ODD = 3 };
 
 template <typename T>
 __device__ __forceinline__ T fp8_out(float v);
@@ -190,7 +196,37 @@ __device__ __forceinline__ void p8_write_row(TO* d, uint8_t* buf, const float* v
   }
 }
 
-template <typename TO, int BN>
+// What the CTAs of a pair tell one another where both have given up.
+struct P8Leave {
+  uint32_t peer_loads;  // 1 + the stages that the other CTA has filled
+  uint32_t landed;      // (odd CTA) the even one has seen both CTAs' loads land
+};
+// A CTA's loading thread that has given up, `mine` stages filled: returns once both
+// CTAs' loads have landed.  These count on the even CTA's barriers, which expect them
+// in pairs: the halves that one of the two has not issued are evened out.  An other
+// CTA that has not given up has had all its loads consumed, and so has this one; it
+// says nothing, and the wait for its word (which comes within one limit: it waits
+// for what this CTA waited for) runs out.  Off the pair's way out on purpose: one look
+// at a flag between the last two barriers cost small products 0.8 us.
+__device__ __noinline__ void p8_leave(volatile P8Leave* l, uint64_t* full, uint32_t stages,
+                                      uint32_t half, uint32_t rank, uint32_t mine,
+                                      unsigned long long limit_ns) {
+  const uint32_t other_l = mapa_shared(smem_u32(const_cast<P8Leave*>(l)), rank ^ 1u);
+  st_shared_cluster_u32(other_l, mine + 1);
+  const uint64_t t0 = globaltimer_ns();
+  while ((rank == 0 ? l->peer_loads : l->landed) == 0)
+    if (globaltimer_ns() - t0 > 3 * limit_ns) return;
+  if (rank != 0) return;
+  const uint32_t other = l->peer_loads - 1, n = max(mine, other);
+  for (uint32_t i = min(mine, other); i < n; ++i) {
+    if (mine < other) mbar_arrive_expect_tx(&full[i % stages], half);
+    else mbar_complete_tx(&full[i % stages], half);
+  }
+  ring_land(full, stages, n, limit_ns);
+  st_shared_cluster_u32(other_l + 4, 1);
+}
+
+template <typename TO, int BN, bool HOLD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
     k_fp8_pair(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                const __grid_constant__ CUtensorMap mapD, const __grid_constant__ Fp8Gemm g) {
@@ -208,6 +244,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
   uint64_t* drain = tempty + C::BUFS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile P8Leave* leave = reinterpret_cast<volatile P8Leave*>(tmem_slot + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_cta_rank();
@@ -227,6 +264,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
     mbar_init(&drain[0], 1);
     mbar_init(&drain[1], 1);
     *abort_flag = 0;
+    leave->peer_loads = leave->landed = 0;
     fence_mbar_init();
     tma_prefetch_desc(&mapA);
     tma_prefetch_desc(&mapB);
@@ -246,14 +284,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
   if (warp < 4) {
     reg_dealloc<56>();
     if (warp == 0 && lane == 0) {
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
+      const uint32_t stop =
+          HOLD && g.hold == (leader ? FP8_HOLD_LOAD : FP8_HOLD_LOAD_ODD) ? g.hold_at : ~0u;
+      int stage = 0;
+      uint32_t phase = 0, issued = 0;
       bool ok = true;
       for (int t = pair; t < tiles && ok; t += pairs) {
         const int m0 = (t % g.m_tiles) * 256 + static_cast<int>(rank) * 128;
         const int n0 = (t / g.m_tiles) * BN + static_cast<int>(rank) * C::HN;
         for (int kb = 0; kb < g.KB; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) {
+          if ((HOLD && issued == stop) || !mbar_wait(&empty[stage], phase ^ 1u, wc)) {
             ok = false;
             break;
           }
@@ -269,16 +309,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
           }
         }
       }
-      // every stage this CTA filled has been consumed before it leaves
+      // every stage this CTA filled has been consumed before it leaves, or has landed
       int s = stage;
       uint32_t ph = phase;
-      for (int i = 0; i < C::STAGES && i < issued; ++i) {
+      for (uint32_t i = 0; i < C::STAGES && i < issued; ++i) {
         if (--s < 0) {
           s = C::STAGES - 1;
           ph ^= 1u;
         }
-        mbar_drain_wait(&empty[s], ph, g.wait_limit_ns);
+        if (!mbar_wait(&empty[s], ph, wc)) {
+          ok = false;
+          break;
+        }
       }
+      if (!ok) p8_leave(leave, full, C::STAGES, C::STAGE, rank, issued, g.wait_limit_ns);
     } else if ((warp == 1 || warp == 2) && lane == 0 && leader) {
       // warp 1 the even blocks, warp 2 the odd: their buffers differ, so nothing
       // orders the two, and the waits of one pass while the other's MMAs run
@@ -287,8 +331,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P8_THREADS, 1)
       const uint64_t hi = d0 & ~uint64_t(0xFFFFFFFFu);
       const uint32_t r0 = static_cast<uint32_t>(d0) + ((smem_u32(ring) & 0x3FFFFu) >> 4);
       uint32_t buf = warp - 1;
-      const long long total =
+      long long total =
           static_cast<long long>((tiles - pair + pairs - 1) / pairs) * g.KB;  // of this pair
+      if (HOLD && g.hold == FP8_HOLD_MMA && g.hold_at < total) total = g.hold_at;
       int stage = warp - 1;
       uint32_t phase = 0, tphase = 1;
       for (long long it = warp - 1; it < total; it += 2) {
@@ -470,7 +515,7 @@ __host__ __device__ constexpr size_t s8_smem_fixed(size_t kbs) {
   return (2 * S8_MAX_STAGES + 2 * S8_BUFS + 2) * 8 + 16 + kbs * BN * 4 + 1024;
 }
 
-template <typename TO, int BN>
+template <typename TO, int BN, bool HOLD>
 __global__ void __launch_bounds__(s8_threads<BN>(), 1)
     k_fp8_skinny(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapW,
                  const __grid_constant__ Fp8Gemm g) {
@@ -532,12 +577,13 @@ __global__ void __launch_bounds__(s8_threads<BN>(), 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
+      const uint32_t stop = HOLD && g.hold == FP8_HOLD_LOAD ? g.hold_at : ~0u;
+      int stage = 0;
+      uint32_t phase = 0, issued = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) {
+          if ((HOLD && issued == stop) || !mbar_wait(&empty[stage], phase ^ 1u, wc)) {
             ok = false;
             break;
           }
@@ -552,15 +598,17 @@ __global__ void __launch_bounds__(s8_threads<BN>(), 1)
           }
         }
       }
+      // every stage has been consumed, or has landed, before the CTA goes on
       int s = stage;
       uint32_t ph = phase;
-      for (int i = 0; i < S && i < issued; ++i) {
+      for (uint32_t i = 0; i < S && i < issued; ++i) {
         if (--s < 0) {
           s = S - 1;
           ph ^= 1u;
         }
-        mbar_drain_wait(&empty[s], ph, g.wait_limit_ns);
+        if (!mbar_wait(&empty[s], ph, wc)) break;
       }
+      if (*abort_flag) ring_land(full, S, issued, g.wait_limit_ns);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -569,13 +617,14 @@ __global__ void __launch_bounds__(s8_threads<BN>(), 1)
       const uint64_t d0 = smem_desc_sw128(0, 16u, 1024u);
       const uint32_t hi = static_cast<uint32_t>(d0 >> 32);
       const uint32_t r0 = static_cast<uint32_t>(d0) + ((smem_u32(ring) & 0x3FFFFu) >> 4);
+      const uint32_t stop = HOLD && g.hold == FP8_HOLD_MMA ? g.hold_at : ~0u;
       int stage = 0;
       uint32_t phase = 0, it = 0;
       bool ok = true;
       for (int t = first; t < tiles && ok; t += step) {
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const uint32_t buf = it % S8_BUFS;
-          if (!mbar_wait(&tempty[buf], ((it / S8_BUFS) & 1) ^ 1u, wc) ||
+          if ((HOLD && it == stop) || !mbar_wait(&tempty[buf], ((it / S8_BUFS) & 1) ^ 1u, wc) ||
               !mbar_wait(&full[stage], phase, wc)) {
             ok = false;
             break;

@@ -86,6 +86,26 @@ __device__ __forceinline__ void mbar_drain_wait(uint64_t* bar, uint32_t parity,
   }
 }
 
+// On the way out after a wait has given up: waits, for at most `limit_ns` in all,
+// until the last loads into a ring of S stages have landed (`issued` so far, in
+// stage order, each completing one phase of its stage's `full`).  The consumer has
+// stopped, so that nothing says when it has read them; its own MMAs it drains.
+__device__ __forceinline__ void ring_land(uint64_t* full, uint32_t S, uint32_t issued,
+                                          unsigned long long limit_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t n = 0; n < S && n < issued; ++n) {
+    const uint32_t i = issued - 1 - n;
+    while (!mbar_try_wait(smem_u32(&full[i % S]), (i / S) & 1))
+      if (globaltimer_ns() - t0 > limit_ns) return;
+  }
+}
+// Counts `bytes` as landed on `bar` that nobody will load.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
+
 // ----------------------------------------------------------------- TMA
 // 1-D bulk copy (no multicast) of `bytes` from global memory into this CTA's
 // shared memory; completion is counted as transaction bytes on `bar`.  Both
@@ -176,6 +196,11 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
 // cluster (cluster-window address).
 __device__ __forceinline__ void st_shared_cluster_u32(uint32_t cluster_addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_cluster_u32(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
 }
 // try_wait with cluster-scope acquire: data another CTA of the cluster wrote
 // before its release-arrive on this barrier is visible afterwards.

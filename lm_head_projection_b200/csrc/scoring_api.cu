@@ -127,8 +127,8 @@ int resident_clusters(int size) {
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  if (!raise_smem(k_fp8_skinny<float, 16>, done) ||
-      cudaOccupancyMaxActiveClusters(&n, k_fp8_skinny<float, 16>, &cfg) != cudaSuccess || n < 1)
+  if (!raise_smem(k_fp8_skinny<float, 16, false>, done) ||
+      cudaOccupancyMaxActiveClusters(&n, k_fp8_skinny<float, 16, false>, &cfg) != cudaSuccess || n < 1)
     n = 1;
   return cache[dev][size] = n;
 }
@@ -140,10 +140,10 @@ struct Fp8Call {
   cudaStream_t st;
 };
 
-template <typename TO, int BN>
+template <typename TO, int BN, bool HOLD>
 flkl_status launch_pair(const Fp8Call& c) {
   static bool done[kMaxDevices];
-  if (!raise_smem(k_fp8_pair<TO, BN>, done)) return FLKL_ERR_CUDA;
+  if (!raise_smem(k_fp8_pair<TO, BN, HOLD>, done)) return FLKL_ERR_CUDA;
   Fp8Gemm g = c.g;
   g.m_tiles = (g.M - 1) / 256 + 1;
   g.n_tiles = (g.N - 1) / BN + 1;
@@ -156,14 +156,14 @@ flkl_status launch_pair(const Fp8Call& c) {
   md = ma;  // (not used where the rows of D are not on 16-byte boundaries)
   if (g.vec && !out_map<TO>(&md, g.D, g.M, g.N)) return FLKL_ERR_CUDA;
   const int pairs = static_cast<int>(std::min<int64_t>(resident_clusters(2), tiles));
-  k_fp8_pair<TO, BN><<<2 * pairs, P8_THREADS, P8<BN>::SMEM, c.st>>>(ma, mb, md, g);
+  k_fp8_pair<TO, BN, HOLD><<<2 * pairs, P8_THREADS, P8<BN>::SMEM, c.st>>>(ma, mb, md, g);
   return launched();
 }
 
-template <typename TO, int BN>
+template <typename TO, int BN, bool HOLD>
 flkl_status launch_skinny(const Fp8Call& c, int cluster) {
   static bool done[kMaxDevices];
-  if (!raise_smem(k_fp8_skinny<TO, BN>, done)) return FLKL_ERR_CUDA;
+  if (!raise_smem(k_fp8_skinny<TO, BN, HOLD>, done)) return FLKL_ERR_CUDA;
   Fp8Gemm g = c.g;
   g.m_tiles = (g.M - 1) / BN + 1;
   g.n_tiles = (g.N - 1) / 128 + 1;
@@ -186,7 +186,7 @@ flkl_status launch_skinny(const Fp8Call& c, int cluster) {
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_fp8_skinny<TO, BN>, mx, mw, g) == cudaSuccess ? FLKL_OK
+  return cudaLaunchKernelEx(&cfg, k_fp8_skinny<TO, BN, HOLD>, mx, mw, g) == cudaSuccess ? FLKL_OK
                                                                                  : FLKL_ERR_CUDA;
 }
 
@@ -195,7 +195,7 @@ flkl_status launch_skinny(const Fp8Call& c, int cluster) {
 // hold 4 or 8 of the small kernel's 128 x 64 ones on two SMs and take about as long
 // per block of K: they win from a dozen large tiles on (256 x 4096 x 4096, 16
 // tiles: 18.8 against 23.5 us; 129 x 1000 x 8192, 4 tiles: 36 against 18 us).
-template <typename TO>
+template <typename TO, bool HOLD>
 flkl_status fp8_matmul(const Fp8Call& c) {
   const int M = c.g.M, KB = c.g.KB, sms = device_sms();
   const int64_t pair_tiles = int64_t((M - 1) / 256 + 1) * ((c.g.N - 1) / 256 + 1);
@@ -208,16 +208,16 @@ flkl_status fp8_matmul(const Fp8Call& c) {
     // (the tokens' scales have to leave room for a ring, which later holds the
     // cluster's parts)
     if (s8_smem_fixed<64>((KB + cluster - 1) / cluster) + 4 * s8_stage_bytes<64>() <= kMaxSmem) {
-      if (M <= 16) return launch_skinny<TO, 16>(c, cluster);
-      if (M <= 32) return launch_skinny<TO, 32>(c, cluster);
-      return launch_skinny<TO, 64>(c, cluster);
+      if (M <= 16) return launch_skinny<TO, 16, HOLD>(c, cluster);
+      if (M <= 32) return launch_skinny<TO, 32, HOLD>(c, cluster);
+      return launch_skinny<TO, 64, HOLD>(c, cluster);
     }
   }
   // Tiles of 128 weight rows where they all run at once: a wave of them takes 0.7
   // of the larger ones' (300 x 4096 x 4096: 18.8 against 24.2 us; two waves of them
   // against one lose: 777 x 4096 x 4096 28.7 against 24.6).
-  if (pair_tiles <= resident_clusters(2) / 2) return launch_pair<TO, 128>(c);
-  return launch_pair<TO, 256>(c);
+  if (pair_tiles <= resident_clusters(2) / 2) return launch_pair<TO, 128, HOLD>(c);
+  return launch_pair<TO, 256, HOLD>(c);
 }
 
 // --------------------------------------------------------- log-probabilities
@@ -250,6 +250,40 @@ flkl_status launch_logprobs(const LpFwdArgs& a, cudaStream_t st) {
   return launch_logprobs_nt<T, TOP, 256>(a, parts, st);
 }
 
+// flkl_fp8_block_matmul, with a role of its kernels that stops after a number of blocks.
+flkl_status block_matmul(const void* A, const float* a_scale, const void* B, const float* b_scale,
+                         const void* bias, int64_t M, int64_t N, int64_t K, int out_dtype, void* D,
+                         void* stream, unsigned long long limit_ns, int hold, uint32_t hold_at) {
+  if (!dtype_ok(out_dtype) || M < 0 || N < 0 || K < 1) return FLKL_ERR_INVALID_ARG;
+  if (K % 16 != 0 || M > kMaxDim / 2 || N > kMaxDim / 2 || K > kMaxDim / 2)
+    return FLKL_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return FLKL_OK;
+  if (A == nullptr || B == nullptr || a_scale == nullptr || b_scale == nullptr || D == nullptr)
+    return FLKL_ERR_INVALID_ARG;
+  const size_t e = elem_size(out_dtype);
+  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(D, e) || !aligned(a_scale, 4) ||
+      !aligned(b_scale, 4) || !aligned(bias, e))
+    return FLKL_ERR_UNSUPPORTED;
+  Fp8Call c{};
+  c.A = A;
+  c.B = B;
+  c.K = K;
+  c.st = static_cast<cudaStream_t>(stream);
+  c.g.sa = a_scale;
+  c.g.sb = b_scale;
+  c.g.bias = bias;
+  c.g.D = D;
+  c.g.M = static_cast<int>(M);
+  c.g.N = static_cast<int>(N);
+  c.g.KB = static_cast<int>((K + kScaleBlock - 1) / kScaleBlock);
+  c.g.wait_limit_ns = limit_ns;
+  c.g.hold = hold;
+  c.g.hold_at = hold_at;
+  if (hold != FP8_HOLD_NONE) return fp8_matmul<__nv_bfloat16, true>(c);
+  return out_dtype == FLKL_DTYPE_BF16 ? fp8_matmul<__nv_bfloat16, false>(c)
+                                      : fp8_matmul<float, false>(c);
+}
+
 }  // namespace
 }  // namespace flkl
 
@@ -274,30 +308,18 @@ flkl_status flkl_fp8_quantize(const void* src, int64_t rows, int64_t cols, int d
 flkl_status flkl_fp8_block_matmul(const void* A, const float* a_scale, const void* B,
                                   const float* b_scale, const void* bias, int64_t M, int64_t N,
                                   int64_t K, int out_dtype, void* D, void* stream) {
-  if (!dtype_ok(out_dtype) || M < 0 || N < 0 || K < 1) return FLKL_ERR_INVALID_ARG;
-  if (K % 16 != 0 || M > kMaxDim / 2 || N > kMaxDim / 2 || K > kMaxDim / 2)
-    return FLKL_ERR_UNSUPPORTED;
-  if (M == 0 || N == 0) return FLKL_OK;
-  if (A == nullptr || B == nullptr || a_scale == nullptr || b_scale == nullptr || D == nullptr)
+  return block_matmul(A, a_scale, B, b_scale, bias, M, N, K, out_dtype, D, stream,
+                      g_wait_limit_ns, FP8_HOLD_NONE, 0);
+}
+
+flkl_status flkl_fp8_wait_selftest(const void* A, const float* a_scale, const void* B,
+                                   const float* b_scale, int64_t M, int64_t N, int64_t K, void* D,
+                                   int role, unsigned int blocks, unsigned int limit_ms,
+                                   void* stream) {
+  if (role < FP8_HOLD_MMA || role > FP8_HOLD_LOAD_ODD || limit_ms < 1 || limit_ms > 1000)
     return FLKL_ERR_INVALID_ARG;
-  const size_t e = elem_size(out_dtype);
-  if (!aligned(A, 16) || !aligned(B, 16) || !aligned(D, e) || !aligned(a_scale, 4) ||
-      !aligned(b_scale, 4) || !aligned(bias, e))
-    return FLKL_ERR_UNSUPPORTED;
-  Fp8Call c{};
-  c.A = A;
-  c.B = B;
-  c.K = K;
-  c.st = static_cast<cudaStream_t>(stream);
-  c.g.sa = a_scale;
-  c.g.sb = b_scale;
-  c.g.bias = bias;
-  c.g.D = D;
-  c.g.M = static_cast<int>(M);
-  c.g.N = static_cast<int>(N);
-  c.g.KB = static_cast<int>((K + kScaleBlock - 1) / kScaleBlock);
-  c.g.wait_limit_ns = g_wait_limit_ns;
-  return out_dtype == FLKL_DTYPE_BF16 ? fp8_matmul<__nv_bfloat16>(c) : fp8_matmul<float>(c);
+  return block_matmul(A, a_scale, B, b_scale, nullptr, M, N, K, FLKL_DTYPE_BF16, D, stream,
+                      limit_ms * 1000000ull, role, blocks);
 }
 
 flkl_status flkl_fp8_device_status(void* stream) {

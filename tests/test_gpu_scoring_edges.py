@@ -1,5 +1,6 @@
 """Edges of the scoring path on the GPU, beside tests/test_gpu_scoring.py: codes at
-exact ties, log-probabilities where logits over temperature leave fp32."""
+exact ties, log-probabilities where logits over temperature leave fp32, waits of
+the product that run out."""
 
 from __future__ import annotations
 
@@ -7,6 +8,7 @@ import numpy as np
 import pytest
 import torch
 
+import lm_head_projection_b200 as pkg
 from oracle import scoring_oracle as o
 from tests.test_gpu_scoring import DT, HALF, U, _close, _np, tol
 
@@ -153,3 +155,46 @@ def test_logprobs_of_rows_far_beyond_the_temperature(dtype, V, m, T):
         # numbers may be cut
         _close(_np(dz), wz, np.abs(wz) * HALF[dtype] + mag * (4 * tol(V) + 1200 * U)
                + 2.0 ** -126, "dz")
+
+
+# ------------------------------------------------- waits of the product that run out
+def _product_inputs(M, N, K, seed=0):
+    from lm_head_projection_b200 import fp8
+
+    g = torch.Generator(device="cuda").manual_seed(seed + M + 3 * N + 5 * K)
+    qa, sa = fp8.quantize_rows(torch.randn(M, K, device="cuda", generator=g))
+    qb, sb = fp8.quantize_blocks(torch.randn(N, K, device="cuda", generator=g))
+    return qa, sa, qb, sb
+
+
+@pytest.mark.parametrize("role", [1, 2, 3])
+@pytest.mark.parametrize("M,N,K,at", [
+    (5, 1000, 2048, 0), (5, 1000, 2048, 1),          # small kernel, clusters that share K
+    (40, 40000, 2048, 0), (40, 40000, 2048, 21),     # several tiles a CTA
+    (300, 2600, 2048, 0), (300, 2600, 2048, 3), (300, 2600, 2048, 9),     # pairs, 128 wide
+    (3000, 5004, 2048, 1), (3000, 5004, 2048, 6), (3000, 5004, 2048, 20)])  # 256 wide
+def test_a_product_whose_waits_run_out(M, N, K, at, role):
+    """One role stops: the others give up after their limit, the kernel ends in
+    good time, says so once, and the next product is right."""
+    from lm_head_projection_b200 import fp8
+
+    qa, sa, qb, sb = _product_inputs(M, N, K)
+    want = fp8.block_matmul(qa, sa, qb, sb)
+    assert pkg.flkl_fp8_device_status() == 0
+    d = torch.zeros_like(want)
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    st = torch.cuda.current_stream().cuda_stream
+    a.record()
+    assert pkg.flkl_fp8_wait_selftest(qa.data_ptr(), sa.data_ptr(), qb.data_ptr(), sb.data_ptr(),
+                                      M, N, K, d.data_ptr(), role, at, 20, st) == 0
+    b.record()
+    status = pkg.flkl_fp8_device_status(st)
+    if M <= 64 and role == 3:  # the small kernel has no odd CTAs
+        assert status == 0 and torch.equal(d, want)
+    else:
+        assert status == 4  # FLKL_ERR_TIMEOUT
+        # a wait, the others' (which begin by then), and the loads' landing
+        assert 15 < a.elapsed_time(b) < 100
+    assert pkg.flkl_fp8_device_status(st) == 0
+    assert torch.equal(fp8.block_matmul(qa, sa, qb, sb), want)
+    assert pkg.flkl_fp8_device_status(st) == 0

@@ -6,8 +6,15 @@ from __future__ import annotations
 from fractions import Fraction
 
 import numpy as np
+import pytest
+import torch
 
+import lm_head_projection_b200 as pkg
 from oracle import scoring_oracle as o
+
+no_gpu = pytest.mark.skipif(torch.cuda.is_available(),
+                            reason="placeholder pointers must not reach a real device")
+P = 4096  # placeholder, 16-byte aligned, never dereferenced
 
 
 def _nearest_e4m3(q: Fraction) -> float:
@@ -33,3 +40,11 @@ def test_exact_quotients_against_fractions():
         assert g == _nearest_e4m3(448 * Fraction(float(x)) / Fraction(float(d))), (x, d)
     # ties go to even: 17 / 448 of the largest lies between codes 16 and 18
     assert o.e4m3_quotients(17.0, 448.0) == 16 and o.e4m3_quotients(-19.0, 448.0) == -20
+
+
+@no_gpu
+def test_wait_selftest_refusals():
+    f = lambda role=1, ms=20, K=64, D=P: pkg.flkl_fp8_wait_selftest(P, P, P, P, 4, 8, K, D, role,
+                                                                   0, ms, 0)
+    assert f(role=0) == 1 and f(role=4) == 1 and f(ms=0) == 1 and f(ms=1001) == 1
+    assert f(K=24) == 2 and f(D=0) == 1
