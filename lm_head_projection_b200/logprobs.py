@@ -81,8 +81,9 @@ def token_logprobs_backward(logits: torch.Tensor, target: Optional[torch.Tensor]
                             dtop_logp: Optional[torch.Tensor] = None, ignore_index: int = -100,
                             temperature: float = 1.0,
                             stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
-    """The gradient of the logits (their type and row stride) for upstream
-    fp32 gradients of logp, entropy ``[rows]`` and top_logp ``[rows, top_k]``
+    """The gradient of the logits (their type, ``[rows, V]``; where the logits'
+    rows start off the 16-byte boundaries, its rows do so alike, a few elements
+    apart) for upstream fp32 gradients of logp, entropy ``[rows]`` and top_logp ``[rows, top_k]``
     (None: none), from the dict that :func:`token_logprobs_forward` returned
     for the same logits, target, ignore_index and temperature."""
     if stream is not None:
@@ -107,11 +108,14 @@ def token_logprobs_backward(logits: torch.Tensor, target: Optional[torch.Tensor]
         if not k:
             raise ValueError("dtop_logp needs alternatives (top_k > 0)")
         _check_dev("dtop_logp", dtop_logp, f32, (rows, k), dev)
-    dlogits = logits.new_empty_strided((rows, V), (ld, 1))
+    # rows one after another, not as far apart as the logits' (which may be one
+    # position of many); the same phase within 16 bytes keeps the vector path
+    dld = V + (ld - V) % (16 // logits.element_size())
+    dlogits = logits.new_empty_strided((rows, V), (dld, 1))
     _launch("flkl_token_logprobs_backward", dev, logits.data_ptr(), ld, _ptr(target),
             ignore_index, rows, V, DTYPES[logits.dtype], temperature, k, stats.data_ptr(),
             entropy.data_ptr(), _ptr(top_ids), _ptr(dlogp), _ptr(dentropy), _ptr(dtop_logp),
-            dlogits.data_ptr(), ld)
+            dlogits.data_ptr(), dld)
     return dlogits
 
 

@@ -198,3 +198,32 @@ def test_a_product_whose_waits_run_out(M, N, K, at, role):
     assert pkg.flkl_fp8_device_status(st) == 0
     assert torch.equal(fp8.block_matmul(qa, sa, qb, sb), want)
     assert pkg.flkl_fp8_device_status(st) == 0
+
+
+# ------------------------------------------------------ gradients of spread rows
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("V,between", [(3000, 64), (3001, 7), (2999, 1), (3000, 100)])
+def test_logprobs_gradient_of_one_position_of_many(dtype, V, between):
+    """``logits[:, -1]`` of a batch of sequences: the gradient takes rows times V,
+    not the whole sequences' memory, and holds the dense rows' bits."""
+    from lm_head_projection_b200 import logprobs
+
+    g = torch.Generator().manual_seed(V)
+    z = torch.randn(6, between, V, generator=g).to(DT[dtype]).cuda()
+    last = z[:, -1]
+    assert between == 1 or not last.is_contiguous()
+    t = torch.randint(0, V, (6,), generator=g).cuda()
+    gl, ge = torch.randn(6, generator=g).cuda(), torch.randn(6, generator=g).cuda()
+    f = logprobs.token_logprobs_forward(last, t)
+    d = logprobs.token_logprobs_backward(last, t, f, dlogp=gl, dentropy=ge)
+    assert d.shape == last.shape and d.stride(1) == 1 and V <= d.stride(0) < V + 8
+    assert d.untyped_storage().nbytes() <= 6 * (V + 8) * z.element_size()
+    dense = last.contiguous()
+    want = logprobs.token_logprobs_backward(dense, t, f, dlogp=gl, dentropy=ge)
+    assert torch.equal(d, want)
+    # through autograd, into the whole tensor
+    z.requires_grad_()
+    r = logprobs.token_logprobs(z[:, -1], t)
+    ((r.logp * gl).sum() + (r.entropy * ge).sum()).backward()
+    assert torch.equal(z.grad[:, -1], want)
+    assert between == 1 or (z.grad[:, :-1] == 0).all()
