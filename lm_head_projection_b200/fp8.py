@@ -94,25 +94,31 @@ class Fp8Head(torch.nn.Module):
 
     ``forward(hidden)`` quantises the rows of ``hidden [..., H]`` and gives
     their logits; ``logits(codes, scale)`` takes rows that are quantised
-    already (the norm's 8-bit output).  ``bias [V]`` is kept in ``out_dtype``."""
+    already (the norm's 8-bit output), and another ``out_dtype`` than the head's
+    where the caller wants one.  ``bias [V]`` (float32 or bfloat16) keeps its type
+    and is cast to that of the logits where they differ."""
 
     def __init__(self, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
                  out_dtype: torch.dtype = torch.bfloat16):
         super().__init__()
         if out_dtype not in DTYPES:
             raise ValueError(f"out_dtype {out_dtype} not supported (float32 or bfloat16)")
+        if bias is not None and bias.dtype not in DTYPES:
+            bias = bias.to(out_dtype)
         codes, scale = quantize_blocks(weight.detach().contiguous())
         self.register_buffer("codes", codes)
         self.register_buffer("scale", scale)
-        self.register_buffer("bias", None if bias is None
-                             else bias.detach().to(out_dtype).contiguous())
+        self.register_buffer("bias", None if bias is None else bias.detach().contiguous())
         self.out_dtype = out_dtype
 
     def logits(self, codes: torch.Tensor, scale: torch.Tensor,
-               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+               out: Optional[torch.Tensor] = None,
+               out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
         K = self.codes.shape[1]
+        dt = self.out_dtype if out_dtype is None else out_dtype
         D = block_matmul(codes.reshape(-1, K), scale.reshape(-1, self.scale.shape[1]),
-                         self.codes, self.scale, self.bias, self.out_dtype, out)
+                         self.codes, self.scale,
+                         None if self.bias is None else self.bias.to(dt), dt, out)
         return D.reshape(*codes.shape[:-1], D.shape[-1])
 
     @torch.no_grad()

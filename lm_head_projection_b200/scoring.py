@@ -22,7 +22,9 @@ class Fp8Scorer(torch.nn.Module):
     ``forward(x, residual=None, target=None)`` with ``x [..., H]`` adds the
     residual, norms to e4m3, forms ``block_rows`` rows of logits at a time and
     returns ``{"logp", "entropy", "top_logp", "top_ids", "H"}`` of x's leading
-    shape (None for what was not asked for).  No gradient."""
+    shape (None for what was not asked for).  The logits, which nobody else sees,
+    are fp32 whatever the head's ``out_dtype`` (a bf16 logit of 20 is off by up to
+    0.06, and its log-probability with it).  No gradient."""
 
     def __init__(self, norm: AddRMSNorm, head: Fp8Head, top_k: int = 0,
                  temperature: float = 1.0, ignore_index: int = -100, block_rows: int = 1024):
@@ -45,7 +47,7 @@ class Fp8Scorer(torch.nn.Module):
         parts = []
         for r0 in range(0, max(rows, 1), self.block_rows):
             r1 = min(rows, r0 + self.block_rows)
-            z = self.head.logits(codes[r0:r1], scale[r0:r1])
+            z = self.head.logits(codes[r0:r1], scale[r0:r1], out_dtype=torch.float32)
             parts.append(token_logprobs_forward(z, None if y is None else y[r0:r1],
                                                 self.ignore_index, self.temperature, self.top_k))
         out = {"H": h}

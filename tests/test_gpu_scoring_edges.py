@@ -227,3 +227,42 @@ def test_logprobs_gradient_of_one_position_of_many(dtype, V, between):
     ((r.logp * gl).sum() + (r.entropy * ge).sum()).backward()
     assert torch.equal(z.grad[:, -1], want)
     assert between == 1 or (z.grad[:, :-1] == 0).all()
+
+
+# ------------------------------------------------------------ the scorer's logits
+@pytest.mark.parametrize("head_dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("bias", [None, "fp32", "bf16"])
+def test_scorer_scores_from_unrounded_logits(head_dtype, bias):
+    """Whatever type the head gives its logits in, the scorer's log-probabilities
+    are those of the fp32 product of the kernels' own codes."""
+    from lm_head_projection_b200.fp8 import Fp8Head
+    from lm_head_projection_b200.norm import AddRMSNorm
+    from lm_head_projection_b200.scoring import Fp8Scorer
+
+    H, V, rows = 512, 3000, 30
+    g = torch.Generator().manual_seed(4)
+    n = AddRMSNorm(H, device="cuda")
+    b = None if bias is None else (torch.randn(V, generator=g) * 3).to(DT[bias]).cuda()
+    w = (torch.randn(V, H, generator=g) * 0.4).bfloat16().cuda()  # logits of 9 and more
+    head = Fp8Head(w, b, out_dtype=DT[head_dtype])
+    x, r = (torch.randn(rows, H, generator=g).bfloat16().cuda() for _ in range(2))
+    t = torch.randint(0, V, (rows,), generator=g).cuda()
+    out = Fp8Scorer(n, head, block_rows=16)(x, r, t)
+    q, s, _ = n.quantized(x, r)
+    z, mag = o.block_matmul(_np(q.float()), _np(s), _np(head.codes.float()), _np(head.scale),
+                            _np(b))
+    want = o.token_logprobs(z, t.cpu().numpy())
+    # the product: 128 + 8 roundings of a step within a block, then its scales and
+    # the blocks' sum, each of the magnitudes at most
+    dz = ((mag + (0 if b is None else np.abs(_np(b)))) * 2 * (136 + 8) * U).max()
+    assert 2 * dz < 0.01  # (bf16 logits of 16 are off by up to 0.06)
+    _close(_np(out["logp"]), want["logp"], 2 * dz + 4 * tol(V))
+    _close(_np(out["entropy"]), want["entropy"], 2 * dz * (2 + np.log(V)) + 30 * tol(V))
+    # the head itself answers in its own type, and in another on request
+    zh = head.logits(q, s)
+    assert zh.dtype == DT[head_dtype]
+    z32 = head.logits(q, s, out_dtype=torch.float32)
+    assert z32.dtype == torch.float32
+    _close(_np(z32), z, dz)
+    if b is None or bias == head_dtype:
+        assert torch.equal(zh, z32.to(DT[head_dtype]))
