@@ -501,6 +501,14 @@ def _launch(what: str, dev, *args) -> None:
         raise FlklError(status, what)
 
 
+def _written(t: torch.Tensor) -> None:
+    """Tells autograd that the library has written over the caller's ``t``: a
+    backward that saved it raises instead of reading the new values.  (Inference
+    tensors have no version to count.)"""
+    if not t.is_inference():
+        torch.autograd.graph.increment_version(t)
+
+
 def _outputs(out: Optional[dict], dev, BT: int, H: int, V: int, dt, pdt, compute_dW: bool,
              compute_db: bool) -> tuple:
     """loss, dX, dW, db for one call: each caller-supplied tensor of ``out``

@@ -14,7 +14,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import DTYPES, _check_dev, _launch, _ptr
+from . import DTYPES, _check_dev, _launch, _ptr, _written
 
 __all__ = ["quantize_rows", "quantize_blocks", "block_matmul", "Fp8Head"]
 
@@ -62,7 +62,9 @@ def block_matmul(A: torch.Tensor, a_scale: torch.Tensor, B: torch.Tensor, b_scal
     """``D = A Bᵀ (+ bias)`` of e4m3 matrices ``A [M, K]`` (scales
     ``[M, ceil(K / 128)]``) and ``B [N, K]`` (scales ``[ceil(N / 128),
     ceil(K / 128)]``), in ``out_dtype`` (bfloat16 or float32; ``bias [N]`` has
-    it too); fp32 sums, one rounding.  K must be a multiple of 16."""
+    it too); fp32 sums, one rounding.  K must be a multiple of 16.  ``out`` is
+    written as by an in-place operation of torch's: it must not require a gradient
+    while gradients are recorded."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return block_matmul(A, a_scale, B, b_scale, bias, out_dtype, out)
@@ -80,12 +82,17 @@ def block_matmul(A: torch.Tensor, a_scale: torch.Tensor, B: torch.Tensor, b_scal
     _check_dev("b_scale", b_scale, torch.float32, (-(-N // 128), kb), dev)
     if bias is not None:
         _check_dev("bias", bias, out_dtype, (N,), dev)
-    if out is None:
+    given = out is not None
+    if not given:
         out = A.new_empty((M, N), dtype=out_dtype)
     else:
         _check_dev("out", out, out_dtype, (M, N), dev)
+        if out.requires_grad and torch.is_grad_enabled():
+            raise ValueError("out requires a gradient")
     _launch("flkl_fp8_block_matmul", dev, A.data_ptr(), a_scale.data_ptr(), B.data_ptr(),
             b_scale.data_ptr(), _ptr(bias), M, N, K, DTYPES[out_dtype], out.data_ptr())
+    if given:
+        _written(out)
     return out
 
 

@@ -24,8 +24,8 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (DTYPES, FLKL_OK, FlklError, _check_dev, _launch, _ptr, flkl_layer_norm_backward,
-               flkl_norm_workspace_size, flkl_rms_norm_backward)
+from . import (DTYPES, FLKL_OK, FlklError, _check_dev, _launch, _ptr, _written,
+               flkl_layer_norm_backward, flkl_norm_workspace_size, flkl_rms_norm_backward)
 
 __all__ = ["rms_norm_backward", "layer_norm_backward", "RMSNorm", "LayerNorm", "add_rms_norm",
            "add_rms_norm_backward", "AddRMSNorm"]
@@ -95,7 +95,9 @@ def add_rms_norm(X: torch.Tensor, W: torch.Tensor, residual: Optional[torch.Tens
     ``quantize`` gives Y as ``torch.float8_e4m3fn`` codes with fp32 scales
     ``[..., ceil(H / 128)]`` (largest magnitude of 128 columns / 448); else Y
     has X's type and scale is None.  Without a residual H is X itself;
-    ``inplace`` writes h over the residual.  No gradient is recorded: see
+    ``inplace`` writes h over the residual, which autograd takes as an in-place
+    change of it (a backward that saved it raises), and is refused for one that
+    requires a gradient while gradients are recorded.  No gradient is recorded: see
     :class:`AddRMSNorm`."""
     if stream is not None:
         with torch.cuda.stream(stream):
@@ -112,6 +114,8 @@ def add_rms_norm(X: torch.Tensor, W: torch.Tensor, residual: Optional[torch.Tens
     Hs = None
     if residual is not None:
         _check_dev("residual", residual, dt, X.shape, dev)
+        if inplace and residual.requires_grad and torch.is_grad_enabled():
+            raise ValueError("inplace would overwrite a residual that requires a gradient")
         Hs = residual.detach() if inplace else torch.empty_like(X)
     elif inplace:
         raise ValueError("inplace needs a residual")
@@ -119,6 +123,8 @@ def add_rms_norm(X: torch.Tensor, W: torch.Tensor, residual: Optional[torch.Tens
     scale = X.new_empty((*X.shape[:-1], -(-H // 128)), dtype=torch.float32) if quantize else None
     _launch("flkl_add_rms_norm_forward", dev, X.data_ptr(), _ptr(residual), W.data_ptr(), rows,
             H, DTYPES[dt], eps, 1 if quantize else 0, Y.data_ptr(), _ptr(scale), _ptr(Hs))
+    if inplace:
+        _written(residual)
     return {"Y": Y, "scale": scale, "H": X if Hs is None else Hs}
 
 

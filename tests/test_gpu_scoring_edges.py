@@ -266,3 +266,53 @@ def test_scorer_scores_from_unrounded_logits(head_dtype, bias):
     _close(_np(z32), z, dz)
     if b is None or bias == head_dtype:
         assert torch.equal(zh, z32.to(DT[head_dtype]))
+
+
+# ------------------------------------------------ what is written over, and autograd
+def test_a_backward_that_saved_what_was_overwritten_raises():
+    """The residual of an in-place norm and the ``out`` of a product count as
+    changed, views of them too."""
+    from lm_head_projection_b200 import fp8, norm
+
+    x, w = torch.randn(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    r = torch.randn(4, 64, device="cuda")
+    a = torch.ones(4, 64, device="cuda", requires_grad=True)
+    y = (a * r).sum()  # saves r
+    norm.add_rms_norm(x, w, r, inplace=True)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    qa, sa, qb, sb = _product_inputs(4, 8, 64)
+    buf = torch.randn(6, 8, device="cuda")
+    b = torch.ones(6, 8, device="cuda", requires_grad=True)
+    y = (b * buf).sum()
+    fp8.block_matmul(qa, sa, qb, sb, out_dtype=torch.float32, out=buf[1:5])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    # not given, nothing counts
+    y = (b * buf).sum()
+    fp8.block_matmul(qa, sa, qb, sb)
+    norm.add_rms_norm(x, w, r)
+    y.backward()
+    with torch.inference_mode():  # tensors without a version
+        r2 = torch.randn(4, 64, device="cuda")
+        h = (x + r2).clone()
+        assert torch.equal(norm.add_rms_norm(x, w, r2, inplace=True)["H"], h)
+        assert torch.equal(r2, h)
+
+
+def test_writing_over_given_tensors_inside_a_graph():
+    from lm_head_projection_b200 import fp8, norm
+
+    x, w = torch.randn(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    r0 = torch.randn(4, 64, device="cuda")
+    r = r0.clone()
+    qa, sa, qb, sb = _product_inputs(4, 8, 64)
+    d = torch.zeros(4, 8, device="cuda", dtype=torch.bfloat16)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        norm.add_rms_norm(x, w, r, inplace=True)
+        fp8.block_matmul(qa, sa, qb, sb, out=d)
+    r.copy_(r0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(r, x + r0) and torch.equal(d, fp8.block_matmul(qa, sa, qb, sb))

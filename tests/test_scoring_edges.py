@@ -48,3 +48,22 @@ def test_wait_selftest_refusals():
                                                                    0, ms, 0)
     assert f(role=0) == 1 and f(role=4) == 1 and f(ms=0) == 1 and f(ms=1001) == 1
     assert f(K=24) == 2 and f(D=0) == 1
+
+
+def test_overwriting_what_requires_a_gradient_is_refused():
+    """Before anything is launched, and only while gradients are recorded."""
+    from lm_head_projection_b200 import fp8, norm
+
+    x, w = torch.zeros(4, 64), torch.ones(64)
+    r = torch.zeros(4, 64, requires_grad=True)
+    with pytest.raises(ValueError, match="requires a gradient"):
+        norm.add_rms_norm(x, w, r, inplace=True)
+    q = torch.zeros(4, 64, dtype=torch.float8_e4m3fn)
+    s1, s2 = torch.ones(4, 1), torch.ones(1, 1)
+    d = torch.zeros(4, 4, requires_grad=True)
+    with pytest.raises(ValueError, match="requires a gradient"):
+        fp8.block_matmul(q, s1, q, s2, out_dtype=torch.float32, out=d)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        norm.add_rms_norm(x, w, r, inplace=True)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        fp8.block_matmul(q, s1, q, s2, out_dtype=torch.float32, out=d)
