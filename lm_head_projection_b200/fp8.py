@@ -103,7 +103,11 @@ class Fp8Head(torch.nn.Module):
     their logits; ``logits(codes, scale)`` takes rows that are quantised
     already (the norm's 8-bit output), and another ``out_dtype`` than the head's
     where the caller wants one.  ``bias [V]`` (float32 or bfloat16) keeps its type
-    and is cast to that of the logits where they differ."""
+    and is cast to that of the logits where they differ.
+
+    ``Module.to`` and its kin move the head between devices; a change of type
+    (``model.to(torch.bfloat16)``, ``.half()``) passes it by, since codes and
+    scales are no numbers of that kind."""
 
     def __init__(self, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
                  out_dtype: torch.dtype = torch.bfloat16):
@@ -117,6 +121,13 @@ class Fp8Head(torch.nn.Module):
         self.register_buffer("scale", scale)
         self.register_buffer("bias", None if bias is None else bias.detach().contiguous())
         self.out_dtype = out_dtype
+
+    def _apply(self, fn, recurse=True):
+        def keep_type(t):
+            probe = fn(t.new_empty(0))
+            return fn(t) if probe.dtype == t.dtype else t.to(probe.device)
+
+        return super()._apply(keep_type, recurse)
 
     def logits(self, codes: torch.Tensor, scale: torch.Tensor,
                out: Optional[torch.Tensor] = None,

@@ -316,3 +316,22 @@ def test_writing_over_given_tensors_inside_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(r, x + r0) and torch.equal(d, fp8.block_matmul(qa, sa, qb, sb))
+
+
+def test_a_head_in_a_model_that_is_cast_and_moved():
+    """The uncast head's bits after .to(dtype), a trip to the host and a new
+    head's load_state_dict."""
+    from lm_head_projection_b200.fp8 import Fp8Head
+
+    w = (torch.randn(1000, 256) * 0.05).cuda()
+    b = torch.randn(1000).cuda()
+    x = torch.randn(9, 256).bfloat16().cuda()
+    head = Fp8Head(w, b)
+    want = head(x)
+    state = {k: v.clone() for k, v in head.state_dict().items()}
+    model = torch.nn.Sequential(head)
+    for m in (model.to(torch.bfloat16), model.half(), model.cpu().cuda(), model.float()):
+        assert torch.equal(m(x), want)
+    other = Fp8Head(torch.zeros_like(w), torch.zeros_like(b))
+    other.load_state_dict(state)
+    assert torch.equal(other(x), want)

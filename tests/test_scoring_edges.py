@@ -67,3 +67,48 @@ def test_overwriting_what_requires_a_gradient_is_refused():
         norm.add_rms_norm(x, w, r, inplace=True)
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
         fp8.block_matmul(q, s1, q, s2, out_dtype=torch.float32, out=d)
+
+
+def _cpu_head(monkeypatch, bias=True):
+    """A head whose codes a stand-in for the quantiser made, since there is no GPU."""
+    from lm_head_projection_b200 import fp8
+
+    g = torch.Generator().manual_seed(1)
+    codes = torch.randn(256, 64, generator=g).to(torch.float8_e4m3fn)
+    scale = torch.rand(2, 1, generator=g) + 0.1
+    monkeypatch.setattr(fp8, "quantize_blocks", lambda w, stream=None: (codes, scale))
+    b = torch.randn(256, generator=g) if bias else None
+    return fp8.Fp8Head(torch.zeros(256, 64), b), codes, scale, b
+
+
+@pytest.mark.parametrize("cast", [
+    lambda m: m.to(torch.bfloat16), lambda m: m.half(), lambda m: m.double(),
+    lambda m: m.float(), lambda m: m.bfloat16(), lambda m: m.to("cpu", torch.float16),
+    lambda m: m.to(torch.zeros(1, dtype=torch.bfloat16)), lambda m: m.cpu()])
+@pytest.mark.parametrize("bias", [True, False])
+def test_a_head_keeps_its_types_under_a_cast_of_the_model(monkeypatch, cast, bias):
+    head, codes, scale, b = _cpu_head(monkeypatch, bias)
+    model = torch.nn.Sequential(torch.nn.Linear(4, 4), head)
+    cast(model)
+    assert head.codes.dtype == torch.float8_e4m3fn and head.scale.dtype == torch.float32
+    assert torch.equal(head.codes.view(torch.uint8), codes.view(torch.uint8))
+    assert torch.equal(head.scale, scale)
+    assert (head.bias is None) if b is None else torch.equal(head.bias, b)
+    # the rest of the model is cast as ever
+    assert model[0].weight.dtype == cast(torch.nn.Linear(1, 1)).weight.dtype
+    # and the state comes back as it went
+    other, *_ = _cpu_head(monkeypatch, bias)
+    other.codes.view(torch.uint8).zero_()
+    other.scale.zero_()
+    other.load_state_dict(head.state_dict())
+    assert torch.equal(other.codes.view(torch.uint8), codes.view(torch.uint8))
+    assert torch.equal(other.scale, scale)
+
+
+def test_a_head_goes_to_another_device(monkeypatch):
+    head, codes, *_ = _cpu_head(monkeypatch)
+    head.to("meta", torch.bfloat16)
+    assert head.codes.device.type == head.scale.device.type == head.bias.device.type == "meta"
+    assert head.codes.dtype == torch.float8_e4m3fn and head.codes.shape == codes.shape
+    head.to_empty(device="cpu")
+    assert head.codes.device.type == "cpu" and head.codes.dtype == torch.float8_e4m3fn
