@@ -19,8 +19,8 @@ class Fp8Scorer(torch.nn.Module):
     """``norm`` (an :class:`~lm_head_projection_b200.norm.AddRMSNorm`) and
     ``head`` (an :class:`~lm_head_projection_b200.fp8.Fp8Head`) as one call:
 
-    ``forward(x, residual=None, target=None)`` with ``x [..., H]`` adds the
-    residual, norms to e4m3, forms ``block_rows`` rows of logits at a time and
+    ``forward(x, residual=None, target=None)`` with ``x [..., H]`` and a target per
+    row, in row order, adds the residual, norms to e4m3, forms ``block_rows`` rows of logits at a time and
     returns ``{"logp", "entropy", "top_logp", "top_ids", "H"}`` of x's leading
     shape (None for what was not asked for).  The logits, which nobody else sees,
     are fp32 whatever the head's ``out_dtype`` (a bf16 logit of 20 is off by up to
@@ -38,8 +38,10 @@ class Fp8Scorer(torch.nn.Module):
     @torch.no_grad()
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
                 target: Optional[torch.Tensor] = None) -> dict:
-        codes, scale, h = self.norm.quantized(x, residual)
         lead = x.shape[:-1]
+        if target is not None and target.numel() != lead.numel():
+            raise ValueError(f"target has shape {tuple(target.shape)}, expected {tuple(lead)}")
+        codes, scale, h = self.norm.quantized(x, residual)
         codes = codes.reshape(-1, codes.shape[-1])
         scale = scale.reshape(-1, scale.shape[-1])
         y = None if target is None else target.reshape(-1).contiguous()

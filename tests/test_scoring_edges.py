@@ -112,3 +112,17 @@ def test_a_head_goes_to_another_device(monkeypatch):
     assert head.codes.dtype == torch.float8_e4m3fn and head.codes.shape == codes.shape
     head.to_empty(device="cpu")
     assert head.codes.device.type == "cpu" and head.codes.dtype == torch.float8_e4m3fn
+
+
+def test_a_scorer_wants_one_target_per_row():
+    """A longer target would score rows against their neighbours'."""
+    from lm_head_projection_b200 import norm, scoring
+
+    sc = scoring.Fp8Scorer(norm.AddRMSNorm(64), None)
+    x = torch.zeros(2, 5, 64, dtype=torch.bfloat16)
+    for shape in ((2, 6), (11,), (2, 4), (2,), (0,)):
+        with pytest.raises(ValueError, match="target"):
+            sc(x, None, torch.zeros(shape, dtype=torch.int64))
+    for shape in ((2, 5), (10,), (2, 5, 1)):
+        with pytest.raises(ValueError, match="CUDA"):
+            sc(x, None, torch.zeros(shape, dtype=torch.int64))
