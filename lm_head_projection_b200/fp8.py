@@ -27,8 +27,8 @@ def _quantize(x: torch.Tensor, block_rows: int, stream) -> Tuple[torch.Tensor, t
             return _quantize(x, block_rows, None)
     if x.dtype not in DTYPES:
         raise ValueError(f"dtype {x.dtype} not supported (float32 or bfloat16)")
-    if x.dim() < 2:
-        raise ValueError("x needs rows and columns")
+    if x.dim() < 1:
+        raise ValueError("x needs a last dimension")
     _check_dev("x", x, x.dtype, x.shape, x.device)
     K = x.shape[-1]
     rows = x.numel() // K if K else 0
@@ -137,7 +137,7 @@ class Fp8Head(torch.nn.Module):
         D = block_matmul(codes.reshape(-1, K), scale.reshape(-1, self.scale.shape[1]),
                          self.codes, self.scale,
                          None if self.bias is None else self.bias.to(dt), dt, out)
-        return D.reshape(*codes.shape[:-1], D.shape[-1])
+        return D.reshape((*codes.shape[:-1], D.shape[-1]))
 
     @torch.no_grad()
     def forward(self, hidden: torch.Tensor) -> torch.Tensor:

@@ -20,9 +20,9 @@ class Fp8Scorer(torch.nn.Module):
     ``head`` (an :class:`~lm_head_projection_b200.fp8.Fp8Head`) as one call:
 
     ``forward(x, residual=None, target=None)`` with ``x [..., H]`` and a target per
-    row, in row order, adds the residual, norms to e4m3, forms ``block_rows`` rows of logits at a time and
-    returns ``{"logp", "entropy", "top_logp", "top_ids", "H"}`` of x's leading
-    shape (None for what was not asked for).  The logits, which nobody else sees,
+    row, in row order, adds the residual, norms to e4m3, forms ``block_rows`` rows
+    of logits at a time and returns ``{"logp", "entropy", "top_logp", "top_ids",
+    "H"}`` of x's leading shape (None for what was not asked for).  The logits, which nobody else sees,
     are fp32 whatever the head's ``out_dtype`` (a bf16 logit of 20 is off by up to
     0.06, and its log-probability with it).  No gradient."""
 
@@ -59,5 +59,5 @@ class Fp8Scorer(torch.nn.Module):
                 out[n] = None
             else:
                 t = v[0] if len(v) == 1 else torch.cat(v)
-                out[n] = t.reshape(*lead, *t.shape[1:])
+                out[n] = t.reshape((*lead, *t.shape[1:]))
         return out

@@ -335,3 +335,26 @@ def test_a_head_in_a_model_that_is_cast_and_moved():
     other = Fp8Head(torch.zeros_like(w), torch.zeros_like(b))
     other.load_state_dict(state)
     assert torch.equal(other(x), want)
+
+
+def test_one_row_without_leading_dimensions():
+    """``[H]`` in, a number (or ``[top_k]``) out, as the shapes say."""
+    from lm_head_projection_b200 import fp8
+    from lm_head_projection_b200.norm import AddRMSNorm
+    from lm_head_projection_b200.scoring import Fp8Scorer
+
+    H, V = 256, 700
+    n = AddRMSNorm(H, device="cuda")
+    head = fp8.Fp8Head((torch.randn(V, H) * 0.1).cuda())
+    x, r = (torch.randn(3, H).bfloat16().cuda() for _ in range(2))
+    t = torch.tensor([5, 6, 7]).cuda()
+    sc = Fp8Scorer(n, head, top_k=4)
+    want = sc(x, r, t)
+    one = sc(x[1], r[1], t[1])
+    assert one["logp"].shape == one["entropy"].shape == () and one["top_ids"].shape == (4,)
+    assert one["H"].shape == (H,)
+    for k in want:
+        assert torch.equal(one[k], want[k][1]), k
+    q, s = fp8.quantize_rows(x[1])
+    assert q.shape == (H,) and s.shape == (2,)
+    assert torch.equal(head(x[1]), head(x)[1]) and head(x[1]).shape == (V,)
