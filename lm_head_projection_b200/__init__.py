@@ -501,6 +501,15 @@ def _launch(what: str, dev, *args) -> None:
         raise FlklError(status, what)
 
 
+def _on(stream, dev):
+    """``stream`` as the current one, for tensors of ``dev``; a stream of another
+    device is refused (its device would be current, the tensors' work on the
+    stream that happens to be current on theirs)."""
+    if stream.device != dev:
+        raise ValueError(f"the stream is of {stream.device}, the tensors are on {dev}")
+    return torch.cuda.stream(stream)
+
+
 def _written(t: torch.Tensor) -> None:
     """Tells autograd that the library has written over the caller's ``t``: a
     backward that saved it raises instead of reading the new values.  (Inference

@@ -14,7 +14,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import DTYPES, _check_dev, _launch, _ptr, _written
+from . import DTYPES, _check_dev, _launch, _on, _ptr, _written
 
 __all__ = ["quantize_rows", "quantize_blocks", "block_matmul", "Fp8Head"]
 
@@ -23,7 +23,7 @@ _F8 = torch.float8_e4m3fn
 
 def _quantize(x: torch.Tensor, block_rows: int, stream) -> Tuple[torch.Tensor, torch.Tensor]:
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x.device):
             return _quantize(x, block_rows, None)
     if x.dtype not in DTYPES:
         raise ValueError(f"dtype {x.dtype} not supported (float32 or bfloat16)")
@@ -66,7 +66,7 @@ def block_matmul(A: torch.Tensor, a_scale: torch.Tensor, B: torch.Tensor, b_scal
     written as by an in-place operation of torch's: it must not require a gradient
     while gradients are recorded."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, A.device):
             return block_matmul(A, a_scale, B, b_scale, bias, out_dtype, out)
     if out_dtype not in DTYPES:
         raise ValueError(f"out_dtype {out_dtype} not supported (float32 or bfloat16)")

@@ -16,7 +16,7 @@ from typing import NamedTuple, Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import DTYPES, _check_dev, _launch, _ptr
+from . import DTYPES, _check_dev, _launch, _on, _ptr
 
 __all__ = ["token_logprobs_forward", "token_logprobs_backward", "token_logprobs",
            "TokenLogProbs", "TokenLogProbsOutput", "MAX_TOP_K"]
@@ -54,7 +54,7 @@ def token_logprobs_forward(logits: torch.Tensor, target: Optional[torch.Tensor] 
     probability 0; a row of nothing else gives logp, lse and top_logp
     -infinity and entropy 0."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, logits.device):
             return token_logprobs_forward(logits, target, ignore_index, temperature, top_k)
     rows, V, ld = _check_logits(logits, target)
     if not 0 <= top_k <= min(MAX_TOP_K, V):
@@ -87,7 +87,7 @@ def token_logprobs_backward(logits: torch.Tensor, target: Optional[torch.Tensor]
     (None: none), from the dict that :func:`token_logprobs_forward` returned
     for the same logits, target, ignore_index and temperature."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, logits.device):
             return token_logprobs_backward(logits, target, forward, dlogp, dentropy, dtop_logp,
                                            ignore_index, temperature)
     rows, V, ld = _check_logits(logits, target)

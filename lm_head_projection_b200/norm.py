@@ -24,7 +24,7 @@ from typing import Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import (DTYPES, FLKL_OK, FlklError, _check_dev, _launch, _ptr, _written,
+from . import (DTYPES, FLKL_OK, FlklError, _check_dev, _launch, _on, _ptr, _written,
                flkl_layer_norm_backward, flkl_norm_workspace_size, flkl_rms_norm_backward)
 
 __all__ = ["rms_norm_backward", "layer_norm_backward", "RMSNorm", "LayerNorm", "add_rms_norm",
@@ -100,7 +100,7 @@ def add_rms_norm(X: torch.Tensor, W: torch.Tensor, residual: Optional[torch.Tens
     requires a gradient while gradients are recorded.  No gradient is recorded: see
     :class:`AddRMSNorm`."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, X.device):
             return add_rms_norm(X, W, residual, eps, quantize, inplace)
     if X.dtype not in DTYPES:
         raise ValueError(f"dtype {X.dtype} not supported (float32 or bfloat16)")
@@ -136,7 +136,7 @@ def add_rms_norm_backward(dY: torch.Tensor, H: torch.Tensor, W: torch.Tensor,
     and of the residual alike, with ``dH`` (what arrives at h from its other
     use) added; and dW unless the weight is frozen.  Returns ``{"dX", "dW"}``."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, dY.device):
             return add_rms_norm_backward(dY, H, W, dH, eps, compute_dW, accum_fp32)
     rows, hidden, dev, dt, pdt = _prepare(dY, H, W, accum_fp32)
     if dH is not None:

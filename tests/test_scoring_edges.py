@@ -126,3 +126,23 @@ def test_a_scorer_wants_one_target_per_row():
     for shape in ((2, 5), (10,), (2, 5, 1)):
         with pytest.raises(ValueError, match="CUDA"):
             sc(x, None, torch.zeros(shape, dtype=torch.int64))
+
+
+def test_a_stream_of_another_device_is_refused():
+    """Before anything is allocated or launched, by every call that takes one."""
+    from types import SimpleNamespace
+
+    from lm_head_projection_b200 import fp8, logprobs, norm
+
+    st = SimpleNamespace(device=torch.device("cuda:1"))
+    x, w = torch.zeros(4, 64), torch.ones(64)
+    q, s1, s2 = torch.zeros(4, 64, dtype=torch.float8_e4m3fn), torch.ones(4, 1), torch.ones(1, 1)
+    f = dict(stats=torch.zeros(4, 2), entropy=torch.zeros(4), top_ids=None)
+    for call in (lambda: norm.add_rms_norm(x, w, stream=st),
+                 lambda: norm.add_rms_norm_backward(x, x, w, stream=st),
+                 lambda: fp8.quantize_rows(x, stream=st), lambda: fp8.quantize_blocks(x, stream=st),
+                 lambda: fp8.block_matmul(q, s1, q, s2, stream=st),
+                 lambda: logprobs.token_logprobs_forward(x, stream=st),
+                 lambda: logprobs.token_logprobs_backward(x, None, f, stream=st)):
+        with pytest.raises(ValueError, match="stream is of cuda:1"):
+            call()
