@@ -163,7 +163,11 @@ def _product_inputs(M, N, K, seed=0):
 
     g = torch.Generator(device="cuda").manual_seed(seed + M + 3 * N + 5 * K)
     qa, sa = fp8.quantize_rows(torch.randn(M, K, device="cuda", generator=g))
-    qb, sb = fp8.quantize_blocks(torch.randn(N, K, device="cuda", generator=g))
+    qb = torch.empty(N, K, dtype=torch.float8_e4m3fn, device="cuda")
+    sb = torch.empty(-(-N // 128), -(-K // 128), device="cuda")
+    for i in range(0, N, 1280):  # whole blocks of rows at a time
+        qb[i:i + 1280], sb[i // 128:i // 128 + 10] = fp8.quantize_blocks(
+            torch.randn(min(1280, N - i), K, device="cuda", generator=g))
     return qa, sa, qb, sb
 
 
@@ -358,3 +362,49 @@ def test_one_row_without_leading_dimensions():
     q, s = fp8.quantize_rows(x[1])
     assert q.shape == (H,) and s.shape == (2,)
     assert torch.equal(head(x[1]), head(x)[1]) and head(x[1]).shape == (V,)
+
+
+# ------------------------------------------------ deep products, block by block
+def _blockwise(qa, sa, qb, sb):
+    """In 64 bits: the product, and how far fp32 may be off.  A block's 128 products
+    are exact and added in at most 128 + 8 steps of up to 2 U (the tensor cores may
+    cut) of their magnitudes' sum; its scales' product and its addition are off by U
+    each of the result and of the sum so far, which the blocks' magnitudes bound."""
+    M, K = qa.shape
+    N = qb.shape[0]
+    d, inner, outer = (torch.zeros(M, N, dtype=torch.float64, device="cuda") for _ in range(3))
+    per_row = sb.double().repeat_interleave(128, 0)[:N]
+    nb = sa.shape[1]
+    for j in range(nb):
+        a = qa[:, 128 * j:128 * j + 128].double() * sa[:, j:j + 1].double()
+        b = qb[:, 128 * j:128 * j + 128].double() * per_row[:, j:j + 1]
+        p = a @ b.T
+        d += p
+        outer += p.abs()
+        inner += a.abs() @ b.abs().T
+    return d, 2 * (128 + 8) * U * inner + 2 * (nb + 2) * U * outer
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (3, 9601, 67216),                    # too deep for the small kernel: pairs of 3 tokens
+    (1, 300, 14336), (16, 1000, 14352), (40, 20000, 8208),   # small kernel, 16 to 64 columns
+    (129, 300, 14320), (300, 2600, 8208), (1000, 2504, 4112)])
+def test_deep_products_lose_no_block(M, N, K):
+    """Every eighth block of K in turn weighs 256 times the others, the short last
+    one among them: whole outputs, to a bound that any lost block exceeds."""
+    from lm_head_projection_b200 import fp8
+
+    qa, sa, qb, sb = _product_inputs(M, N, K)
+    nb = sa.shape[1]
+    j = torch.arange(nb, device="cuda")
+    for p in range(8):
+        s = torch.where((j % 8 == p) | (j == nb - 1), 256.0, 1.0) * sa
+        want, bound = _blockwise(qa, s, qb, sb)
+        got = fp8.block_matmul(qa, s, qb, sb, out_dtype=torch.float32).double()
+        err = (got - want).abs()
+        assert (err <= bound + want.abs() * U).all(), (p, (err / bound).max())
+        # what one heavy block adds, the smallest of them, is above the bound
+        k0 = 128 * (nb - 1)
+        tail = (qa[:, k0:].double() * s[:, -1:].double()) @ (
+            qb[:, k0:].double() * sb.double().repeat_interleave(128, 0)[:N, -1:]).T
+        assert tail.square().mean().sqrt() > 4 * bound.mean()
