@@ -51,12 +51,15 @@ def rms_norm_backward(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, eps: f
                       stream: Optional[torch.cuda.Stream] = None) -> dict:
     """dX (and dW unless the weight is frozen) of ``y = W * X / rms(X)``
     over the last dimension; returns ``{"dX", "dW"}`` (dW None when frozen)."""
+    if stream is not None:  # what the call allocates belongs to its stream, too
+        with _on(stream, X.device):
+            return rms_norm_backward(dY, X, W, eps, compute_dW, accum_fp32)
     rows, H, dev, dt, pdt = _prepare(dY, X, W, accum_fp32)
     dX = torch.empty_like(X)
     dW = torch.empty((H,), dtype=pdt, device=dev) if compute_dW else None
     need = flkl_norm_workspace_size(rows, H, compute_dW, False)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    st = torch.cuda.current_stream(dev)
     status = flkl_rms_norm_backward(_ptr(dY), _ptr(X), _ptr(W), rows, H, DTYPES[dt], eps,
                                     compute_dW, accum_fp32, _ptr(dX), _ptr(dW), _ptr(ws), need,
                                     st.cuda_stream)
@@ -71,13 +74,16 @@ def layer_norm_backward(dY: torch.Tensor, X: torch.Tensor, W: torch.Tensor, eps:
                         stream: Optional[torch.cuda.Stream] = None) -> dict:
     """dX, dW and db (None when frozen) of ``y = W * (X - mean) / std + b``
     over the last dimension; returns ``{"dX", "dW", "db"}``."""
+    if stream is not None:
+        with _on(stream, X.device):
+            return layer_norm_backward(dY, X, W, eps, compute_dW, compute_db, accum_fp32)
     rows, H, dev, dt, pdt = _prepare(dY, X, W, accum_fp32)
     dX = torch.empty_like(X)
     dW = torch.empty((H,), dtype=pdt, device=dev) if compute_dW else None
     db = torch.empty((H,), dtype=pdt, device=dev) if compute_db else None
     need = flkl_norm_workspace_size(rows, H, compute_dW, compute_db)
     ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    st = torch.cuda.current_stream(dev)
     status = flkl_layer_norm_backward(_ptr(dY), _ptr(X), _ptr(W), rows, H, DTYPES[dt], eps,
                                       compute_dW, compute_db, accum_fp32, _ptr(dX), _ptr(dW),
                                       _ptr(db), _ptr(ws), need, st.cuda_stream)

@@ -408,3 +408,28 @@ def test_deep_products_lose_no_block(M, N, K):
         tail = (qa[:, k0:].double() * s[:, -1:].double()) @ (
             qb[:, k0:].double() * sb.double().repeat_interleave(128, 0)[:N, -1:]).T
         assert tail.square().mean().sqrt() > 4 * bound.mean()
+
+
+# ------------------------------------------- norm backwards on a stream of their own
+def test_norm_backwards_allocate_on_the_stream_they_are_given():
+    """Their workspace is freed on return, while the kernels run: it must not go back
+    to the current stream, which is busy allocating the same size."""
+    from lm_head_projection_b200 import flkl_norm_workspace_size, norm
+
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, dy = (torch.randn(4096, 2048, device="cuda", generator=g) for _ in range(2))
+    w = torch.randn(2048, device="cuda", generator=g)
+    want = [norm.rms_norm_backward(dy, x, w), norm.layer_norm_backward(dy, x, w)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [norm.rms_norm_backward(dy, x, w, stream=side),
+               norm.layer_norm_backward(dy, x, w, stream=side)]
+        for n in (1, 2):
+            torch.full((flkl_norm_workspace_size(4096, 2048, True, n == 2),), 0xFF,
+                       dtype=torch.uint8, device="cuda")
+        side.synchronize()
+        for a, b in zip(got, want):
+            for k in a:
+                assert a[k] is None or torch.equal(a[k], b[k]), k
+    torch.cuda.synchronize()

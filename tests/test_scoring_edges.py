@@ -140,6 +140,8 @@ def test_a_stream_of_another_device_is_refused():
     f = dict(stats=torch.zeros(4, 2), entropy=torch.zeros(4), top_ids=None)
     for call in (lambda: norm.add_rms_norm(x, w, stream=st),
                  lambda: norm.add_rms_norm_backward(x, x, w, stream=st),
+                 lambda: norm.rms_norm_backward(x, x, w, stream=st),
+                 lambda: norm.layer_norm_backward(x, x, w, stream=st),
                  lambda: fp8.quantize_rows(x, stream=st), lambda: fp8.quantize_blocks(x, stream=st),
                  lambda: fp8.block_matmul(q, s1, q, s2, stream=st),
                  lambda: logprobs.token_logprobs_forward(x, stream=st),
