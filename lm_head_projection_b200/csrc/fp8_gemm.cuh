@@ -21,10 +21,11 @@
 // and 256 of additions per SM quarter, which would fit side by side; but a buffer's
 // way round (commit, wake, read, arrival in the other CTA, wake: about 700 clocks
 // beside the 450 of the read) has only two buffers to hide behind, as 512 columns
-// of TMEM hold no third.  1024 x 128256 x 4096 takes 857 clocks a block (635 without
-// additions and stores) and 507 us (2120 TFLOP/s) in a burst; back to back the
-// power limit holds the clock at 1.3 - 1.5 GHz (578 us).  What made it so: two issuing
-// threads instead of one (585 -> 551 us), reads of 16 columns with the next on its
+// of TMEM hold no third of 256 (three of 160 were not measured).  1024 x 128256 x
+// 4096 takes 857 clocks a block (635 without additions and stores) and 490 - 507 us
+// (2120 TFLOP/s and more) in a burst; back to back the power limit holds the clock
+// at 1.3 - 1.5 GHz (577 - 592 us).  What made it so: two issuing threads instead of
+// one (585 -> 551 us), reads of 16 columns with the next on its
 // way (551 -> 528), a relaxed arrival (a cluster-scope release cost 1100 clocks a
 // block), the scales of four blocks in one load.  Measured and left: tokens on the
 // N side (their scales then come from shared memory, 512 bytes a load: 892 us),

@@ -187,7 +187,8 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
 }
 // The same without ordering other CTAs' view of this thread's memory accesses
 // (a cluster-scope release waits for all of them): for handing back TMEM, whose
-// loads tcgen05.wait::ld has seen complete.
+// loads tcgen05.wait::ld has seen complete.  It orders nothing else: a thread that
+// writes something for the other CTA before it needs mbar_arrive_cluster.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");

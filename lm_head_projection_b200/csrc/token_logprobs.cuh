@@ -34,11 +34,13 @@
 // cluster of 2, 4 or 8 CTAs, which leave their sums and k best in shared memory
 // for the first to join, in rank order.
 //
-// Bound by instruction issue and HBM together: an exponential takes 8 clocks of an
-// SM quarter per 32 logits, the rest of a bf16 logit about 7 issue slots (two
-// logits an instruction where there is one).  Measured, 2048 x 128256 bf16 (525 MB):
-// 92 us without alternatives (5.7 TB/s), 106 us with 5, 112 us with 32; 1024 x
-// 128256 fp32: 79 and 91 us (6.6 and 5.8 TB/s).  Four CTAs of 256 threads an SM with
+// Neither issue nor HBM is full (2048 x 128256 bf16 with 5 alternatives: 70 % of
+// issue slots, 55 % of DRAM's peak, where a copy reaches 80): an exponential takes 8
+// clocks of an SM quarter per 32 logits, the rest of a bf16 logit about 7 issue slots
+// (two logits an instruction where there is one), 2048 rows over the 592 places are
+// 3.5 waves with idle ends, and a row's search for alternatives reads nothing ahead.
+// Measured, those rows (525 MB): 88 - 94 us without alternatives (5.6 - 5.9 TB/s),
+// 105 - 111 with 5; 1024 x 128256 fp32: 81 and 92 us (6.5 and 5.7 TB/s).  Four CTAs of 256 threads an SM with
 // the next tile on its way beat five without (97 against 103 us); the alternatives
 // as a running list in the pass, cut as it grew, took 286 us.
 #pragma once

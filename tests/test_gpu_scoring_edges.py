@@ -433,3 +433,33 @@ def test_norm_backwards_allocate_on_the_stream_they_are_given():
             for k in a:
                 assert a[k] is None or torch.equal(a[k], b[k]), k
     torch.cuda.synchronize()
+
+
+# --------------------------------------------------------------- the chain's ends
+def test_scorer_without_rows_and_captured_with_a_bias():
+    from lm_head_projection_b200.fp8 import Fp8Head
+    from lm_head_projection_b200.norm import AddRMSNorm
+    from lm_head_projection_b200.scoring import Fp8Scorer
+
+    H, V = 256, 1000
+    n = AddRMSNorm(H, device="cuda")
+    head = Fp8Head((torch.randn(V, H) * 0.1).cuda(), torch.randn(V).bfloat16().cuda())
+    sc = Fp8Scorer(n, head, top_k=3, block_rows=16)
+    for lead in ((0,), (2, 0)):
+        out = sc(torch.empty(*lead, H).bfloat16().cuda(), None,
+                 torch.empty(lead, dtype=torch.int64, device="cuda"))
+        assert out["logp"].shape == lead and out["top_ids"].shape == (*lead, 3)
+    x = torch.randn(40, H).bfloat16().cuda()
+    t = torch.randint(0, V, (40,)).cuda()
+    want = sc(x, None, t)
+    xs = torch.randn_like(x)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = sc(xs, None, t)
+    xs.copy_(x)
+    g.replay()
+    torch.cuda.synchronize()
+    for k in ("logp", "entropy", "top_logp", "top_ids"):
+        assert torch.equal(out[k], want[k]), k
+    with pytest.raises(ValueError, match="out"):
+        head.logits(*n.quantized(x)[:2], out=torch.empty(40, V, device="cuda"))
