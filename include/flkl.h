@@ -477,13 +477,12 @@ FLKL_API flkl_status flkl_fp8_block_matmul(const void* A, const float* a_scale, 
 FLKL_API flkl_status flkl_fp8_device_status(void* stream);
 
 /* Self-check of the product's bounded waits: flkl_fp8_block_matmul (bf16 D, no
- * bias) with a limit of
- * `limit_ms` (1 .. 1000) for each wait, in which one role of the kernel stops
- * after `blocks` blocks of K, so that the others' waits run out: role 1 the MMAs,
- * 2 the loads, 3 the loads of a CTA pair's odd CTA (more than 64 rows; nothing
- * stops where the small kernel is chosen).  The kernel waits for the loads that
- * it has issued, and ends; D is undefined and flkl_fp8_device_status returns
- * FLKL_ERR_TIMEOUT once.  Blocks that a CTA never reaches stop nothing. */
+ * bias) with a limit of `limit_ms` (1 .. 1000) for each wait, in which one role of
+ * the kernel stops after `blocks` blocks of K, so that the others' waits run out:
+ * role 1 the MMAs, 2 the loads, 3 the loads of a CTA pair's odd CTA (more than 64
+ * rows; nothing stops where the small kernel is chosen).  The kernel waits for the
+ * loads that it has issued, and ends; D is undefined and flkl_fp8_device_status
+ * returns FLKL_ERR_TIMEOUT once.  Blocks that a CTA never reaches stop nothing. */
 FLKL_API flkl_status flkl_fp8_wait_selftest(const void* A, const float* a_scale, const void* B,
                                             const float* b_scale, int64_t M, int64_t N, int64_t K,
                                             void* D, int role, unsigned int blocks,

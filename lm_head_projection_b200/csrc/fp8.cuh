@@ -7,7 +7,7 @@
 // scale 1 and codes 0: its reciprocal scale would overflow.
 //
 // Ties.  bf16 values (and the norm's products h w of two of them) are short, so
-// that 448 v / m lies exactly between two codes time and again (one of 200 values
+// that 448 v / m lies exactly between two codes time and again (one of 170 values
 // of random bf16 rows).  A quotient from a reciprocal is off by up to 2^-22 of
 // itself and would land on either side; it is therefore rounded to 21 bits first,
 // which a tie (5 bits) is the nearest such number to.  Nothing else comes that

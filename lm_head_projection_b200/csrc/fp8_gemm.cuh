@@ -25,9 +25,9 @@
 // 4096 takes 857 clocks a block (635 without additions and stores) and 490 - 507 us
 // (2120 TFLOP/s and more) in a burst; back to back the power limit holds the clock
 // at 1.3 - 1.5 GHz (577 - 592 us).  What made it so: two issuing threads instead of
-// one (585 -> 551 us), reads of 16 columns with the next on its
-// way (551 -> 528), a relaxed arrival (a cluster-scope release cost 1100 clocks a
-// block), the scales of four blocks in one load.  Measured and left: tokens on the
+// one (585 -> 551 us), reads of 16 columns with the next on its way (551 -> 528), a
+// relaxed arrival (a cluster-scope release cost 1100 clocks a block), the scales of
+// four blocks in one load.  Measured and left: tokens on the
 // N side (their scales then come from shared memory, 512 bytes a load: 892 us),
 // 16 epilogue warps, two MMAs of half the width, packed additions, a deeper ring.
 //
@@ -204,8 +204,8 @@ struct P8Leave {
 };
 // A CTA's loading thread that has given up, `mine` stages filled: returns once both
 // CTAs' loads have landed.  These count on the even CTA's barriers, which expect them
-// in pairs: the halves that one of the two has not issued are evened out.  An other
-// CTA that has not given up has had all its loads consumed, and so has this one; it
+// in pairs: the halves that one of the two has not issued are evened out.  If the
+// other CTA has not given up, all its loads have been consumed, and so this one's; it
 // says nothing, and the wait for its word (which comes within one limit: it waits
 // for what this CTA waited for) runs out.  Off the pair's way out on purpose: one look
 // at a flag between the last two barriers cost small products 0.8 us.

@@ -21,7 +21,8 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const T* __restrict__ src
   if (ok) Vec8<T>::load(src + row * cols + c, v);
   const float m = half_warp_max(amax8(v));
   if (!ok) return;
-  *reinterpret_cast<uint2*>(q + row * cols + c) = e4m3_pack8(v, e4m3_tiny(m) ? 1.f : e4m3_inverse(m));
+  *reinterpret_cast<uint2*>(q + row * cols + c) =
+      e4m3_pack8(v, e4m3_tiny(m) ? 1.f : e4m3_inverse(m));
   if (l == 0) scale[row * kb + b] = e4m3_scale(m);
 }
 

@@ -128,7 +128,8 @@ int resident_clusters(int size) {
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   if (!raise_smem(k_fp8_skinny<float, 16, false>, done) ||
-      cudaOccupancyMaxActiveClusters(&n, k_fp8_skinny<float, 16, false>, &cfg) != cudaSuccess || n < 1)
+      cudaOccupancyMaxActiveClusters(&n, k_fp8_skinny<float, 16, false>, &cfg) != cudaSuccess ||
+      n < 1)
     n = 1;
   return cache[dev][size] = n;
 }
@@ -186,8 +187,9 @@ flkl_status launch_skinny(const Fp8Call& c, int cluster) {
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_fp8_skinny<TO, BN, HOLD>, mx, mw, g) == cudaSuccess ? FLKL_OK
-                                                                                 : FLKL_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k_fp8_skinny<TO, BN, HOLD>, mx, mw, g) == cudaSuccess
+             ? FLKL_OK
+             : FLKL_ERR_CUDA;
 }
 
 // Which kernel.  Up to 64 rows there is one token tile and the weight is streamed

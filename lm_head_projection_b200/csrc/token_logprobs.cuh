@@ -40,9 +40,10 @@
 // (two logits an instruction where there is one), 2048 rows over the 592 places are
 // 3.5 waves with idle ends, and a row's search for alternatives reads nothing ahead.
 // Measured, those rows (525 MB): 88 - 94 us without alternatives (5.6 - 5.9 TB/s),
-// 105 - 111 with 5; 1024 x 128256 fp32: 81 and 92 us (6.5 and 5.7 TB/s).  Four CTAs of 256 threads an SM with
-// the next tile on its way beat five without (97 against 103 us); the alternatives
-// as a running list in the pass, cut as it grew, took 286 us.
+// 105 - 111 with 5; 1024 x 128256 fp32: 81 and 92 us (6.5 and 5.7 TB/s).  Four CTAs
+// of 256 threads an SM with the next tile on its way beat five without (97 against
+// 103 us); the alternatives as a running list in the pass, cut as it grew, took
+// 286 us.
 #pragma once
 
 #include "ptx.cuh"

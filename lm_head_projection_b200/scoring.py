@@ -22,9 +22,9 @@ class Fp8Scorer(torch.nn.Module):
     ``forward(x, residual=None, target=None)`` with ``x [..., H]`` and a target per
     row, in row order, adds the residual, norms to e4m3, forms ``block_rows`` rows
     of logits at a time and returns ``{"logp", "entropy", "top_logp", "top_ids",
-    "H"}`` of x's leading shape (None for what was not asked for).  The logits, which nobody else sees,
-    are fp32 whatever the head's ``out_dtype`` (a bf16 logit of 20 is off by up to
-    0.06, and its log-probability with it).  No gradient."""
+    "H"}`` of x's leading shape (None for what was not asked for).  The logits,
+    which nobody else sees, are fp32 whatever the head's ``out_dtype`` (a bf16 logit
+    of 20 is off by up to 0.06, and its log-probability with it).  No gradient."""
 
     def __init__(self, norm: AddRMSNorm, head: Fp8Head, top_k: int = 0,
                  temperature: float = 1.0, ignore_index: int = -100, block_rows: int = 1024):
